@@ -333,6 +333,62 @@ w4a4_status w4a4_gemm_dual_act(const uint8_t* aq, const uint8_t* sfa, const void
                                const float* inv_s_perm, uint8_t* aq_next, uint8_t* sfa_next,
                                void* xo_next, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit floating point (e4m3): the linear layer for projections that do not
+ * stand 4 bits, or that come from a checkpoint in this format.  An activation
+ * row is cut into blocks of 128 columns, a weight matrix into tiles of
+ * 128 x 128; each block has one float32 scale s and its e4m3 codes c stand
+ * for c * s.  Partial blocks at the right and lower edges are allowed.
+ *
+ * Shapes: d_in % 16 == 0, d_out % 16 == 0, d_in <= 65535, d_out <= 2^30; X
+ * rows as elsewhere (bf16, ldx % 8 == 0); pointers 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+
+/* A weight matrix [d_out, d_in] of e4m3 codes, or a stack of `experts` of
+ * them (dense, one after the other; 1 for a plain weight).  Caller-owned. */
+typedef struct w4a4_fp8_weight {
+  int64_t d_in, d_out, experts;
+  uint8_t* q;        /* e4m3 [experts, d_out, d_in] */
+  float* scale;      /* float32 [experts, ceil(d_out/128), ceil(d_in/128)], any finite values */
+} w4a4_fp8_weight;
+
+/* Quantises activations: per token and block of 128 columns
+ *   s = 2^e, e = max(-126, min{e : max|x| <= 448 * 2^e}),  c = e4m3_rn(x / s)
+ * (x / s is exact, so each element is rounded once, ties to even).  A block
+ * holding an infinity or a NaN gets scale NaN and codes 0.  q: e4m3 [T, d]
+ * dense.  scale: float32 [ceil(d/128)][ld_scale], the scale of token t and
+ * block b at b * ld_scale + t; ld_scale is a multiple of 4 and at least T
+ * rounded up to 4 (entries T .. that are written as 0).  Errors: INVALID_ARG
+ * for negative sizes, ldx < d, ld_scale too small or null pointers;
+ * UNSUPPORTED_SHAPE for d % 16, ldx % 8, ld_scale % 4 or alignment. */
+w4a4_status w4a4_fp8_quant_act(const void* X, int64_t T, int64_t d, int64_t ldx, uint8_t* q,
+                               float* scale, int64_t ld_scale, void* stream);
+
+/* Quantises a weight W: bf16 [experts, d_out, d_in] (row stride ldw, experts
+ * d_out * ldw apart) into w->q and w->scale, one scale per 128 x 128 tile by
+ * the rule above.  At most 65535 experts. */
+w4a4_status w4a4_fp8_pack_weight(const void* W, int64_t ldw, const w4a4_fp8_weight* w, void* stream);
+
+/* Y[t, n] = sum_b scale_a[b, t] * scale_w[n/128, b] * sum_{p in block b} a[t, p] w[n, p]
+ * for w->experts == 1: the sums over a block on the tensor cores, the sum over
+ * blocks in float32 in ascending b (few tokens: in up to 8 ascending ranges of
+ * b whose sums are then added in order; a function of the shape alone).  The
+ * product of the two scales is formed first, in float32.  Y: bf16 [T, d_out]
+ * or, with y_f32 != 0, float32; ldy % 8 == 0.  ld_scale as above. */
+w4a4_status w4a4_fp8_gemm(const uint8_t* a, const float* scale_a, int64_t ld_scale, int64_t T,
+                          const w4a4_fp8_weight* w, void* Y, int64_t ldy, int y_f32, void* stream);
+
+/* Bytes of device workspace w4a4_fp8_linear needs for T tokens of d_in columns. */
+w4a4_status w4a4_fp8_workspace_size(int64_t T, int64_t d_in, size_t* bytes);
+
+/* The layer: w4a4_fp8_quant_act into the workspace, then w4a4_fp8_gemm.  The
+ * weight must not be written by work still running on other streams (as for
+ * any call), and may be read before the kernel just before this call's own
+ * second one has ended. */
+w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp8_weight* w,
+                            void* workspace, size_t ws_bytes, void* Y, int64_t ldy, int y_f32,
+                            void* stream);
+
 /* Size of the fixed device scratch array behind w4a4_linear_noalloc. */
 #define W4A4_NOALLOC_SCRATCH_BYTES ((size_t)32 << 20)
 

@@ -1,0 +1,95 @@
+// Device helpers of the 8-bit floating point (e4m3) operators: the e4m3
+// tensor-core instructions, conversions and the power-of-two block scale.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "w4a4_device.cuh"
+
+namespace w4a4 {
+
+constexpr int kFp8Block = 128;        // columns per scale block (and rows, for weights)
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 x e4m3 -> f32, K = 32 per instruction.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4 with e4m3 inputs (format 0) and f32
+// accumulation, both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
+  return (1u << 4)                                   // D format: f32
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(tmap), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t cluster_addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// Four f32 -> four e4m3 codes, element i in byte i: nearest, ties to even,
+// saturating at +-448 (the first source of each cvt lands in the high byte).
+__device__ __forceinline__ uint32_t cvt_e4m3x4(float v0, float v1, float v2, float v3) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
+  return r;
+}
+
+// Block scale of e4m3 codes: s = 2^e with e the smallest integer such that
+// amax <= 448 * 2^e, at least -126.  amax as float bits (sign clear);
+// 448 = 1.75 * 2^8, so e = E - 8, or E - 7 where the mantissa is above 1.75.
+// Returns the biased exponent e + 127 (1 .. 247), or 0 for a block holding an
+// infinity or a NaN: its scale is NaN and all its codes are 0.
+__device__ __forceinline__ uint32_t f8_scale_exp(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return 0u;
+  const int eb = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return eb < 1 ? 1u : static_cast<uint32_t>(eb);
+}
+__device__ __forceinline__ float f8_scale(uint32_t eb) {
+  return __uint_as_float(eb == 0u ? 0x7FC00000u : eb << 23);
+}
+// 2^-e: the product with it is the exact quotient by the scale (0 for a non-finite block)
+__device__ __forceinline__ float f8_inv_scale(uint32_t eb) {
+  return __uint_as_float((254u - eb) << 23);
+}
+
+}  // namespace w4a4

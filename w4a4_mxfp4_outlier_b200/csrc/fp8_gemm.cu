@@ -1,0 +1,676 @@
+// Matrix product of e4m3 operands with one float32 scale per block of 128:
+//
+//   Y[t, n] = sum_kb  sa[kb, t] * sb[n / 128, kb] * sum_{p in kb} a[t, p] w[n, p]
+//
+// The inner sums (128 products) run on the tensor cores (tcgen05 kind::f8f6f4)
+// into tensor memory; the scales are any float32 numbers, which the tensor
+// cores' own block scales (powers of two) cannot hold, so the outer sum is
+// done by the epilogue warps in float32 registers: for every K block they read
+// the block's partial sums from tensor memory and add them, scaled.  Two
+// accumulator buffers in tensor memory let the tensor cores work on the next K
+// block meanwhile.
+//
+// Two kernels:
+//  * fp8_gemm_pair_kernel: CTA pairs (cta_group::2), 256 tokens x 256 channels
+//    per tile, persistent.
+//  * fp8_gemm_few_kernel: for few tokens, where reading the weight is the
+//    work: the weight rows are the MMA's M (128 per CTA), the tokens its N
+//    (16 .. 128), and the CTAs of a cluster split K and join their sums through
+//    distributed shared memory, in the order of the ranks.
+// Every wait is bounded, as in the other kernels of the library.
+#include <cuda.h>
+
+#include "fp8_device.cuh"
+#include "fp8_internal.h"
+
+namespace w4a4 {
+
+// ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+constexpr int F_THREADS = 192;                // producer, MMA, 4 epilogue warps
+constexpr int F_W_BYTES = 128 * 128;          // weight rows x bytes of one K block
+
+template <int N>
+struct FewSmem {
+  // about 96 KB in flight per CTA, two CTAs per SM
+  static constexpr int kStageBytes = F_W_BYTES + N * 128;
+  static constexpr int kStages = N <= 32 ? 5 : (N == 64 ? 4 : 3);
+  // An accumulator buffer is reused two K blocks later, after the epilogue has
+  // read the scales of the first, so two slots more than stages are enough.
+  static constexpr int kSaSlots = kStages + 2;
+  uint8_t stage[kStages][kStageBytes];
+  alignas(16) float sa[kSaSlots][N];
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t sa_full[kSaSlots];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+  static_assert(N * 512 <= kStages * kStageBytes, "the sums fit the ring");
+};
+
+template <int N, bool kF32>
+__global__ void __launch_bounds__(F_THREADS, 2)
+    fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w,
+                        const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ Fp8GemmArgs args) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  using Smem = FewSmem<N>;
+  constexpr int NST = Smem::kStages;
+  constexpr int TCOLS = 2 * N < 32 ? 32 : 2 * N;
+  Smem& sm = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  volatile uint32_t* abort_flag = &sm.abort_flag;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int C = static_cast<int>(gridDim.z);              // cluster = CTAs along z, one K range each
+  const int rank = static_cast<int>(blockIdx.z);
+  const int n0 = blockIdx.x * 128;
+  const int t0 = blockIdx.y * N;
+  const int nt = args.T - t0 < N ? args.T - t0 : N;       // tokens of this tile
+  const int kb0 = static_cast<int>(static_cast<int64_t>(args.nkb) * rank / C);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(args.nkb) * (rank + 1) / C);
+  const int nk = kb1 - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < Smem::kSaSlots; ++s) mbar_init(&sm.sa_full[s], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 4);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0u;
+    fence_barrier_init();
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, TCOLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == 0) {
+    // ============================ TMA producer ============================
+    // In w4a4_fp8_linear the previous kernel is the library's quantiser, which
+    // lets this one start only after everything before it has ended, and which
+    // does not write the weight: the first weight tiles are then fetched
+    // before waiting for it.
+    const uint32_t sa_bytes = static_cast<uint32_t>((nt + 3) & ~3) * 4u;
+    const int early = args.early_weights ? (nk < NST ? nk : NST) : 0;
+    if (elect_one()) {
+      for (int i = 0; i < early; ++i) {
+        mbar_arrive_expect_tx(&sm.full[i], Smem::kStageBytes);
+        tma_load_2d(sm.stage[i], &tm_w, &sm.full[i], (kb0 + i) * 128, n0);
+      }
+    }
+    __syncwarp();
+    pdl_wait();
+    pdl_launch_dependents();
+    uint32_t issued = 0;
+    for (int i = 0; i < nk; ++i) {
+      const int s = i % NST;
+      const int q = i % Smem::kSaSlots;
+      if (i >= NST && !warp_wait_bounded(&sm.empty[s], ((i / NST) & 1) ^ 1u, abort_flag,
+                                         DEVERR_TIMEOUT_PRODUCER))
+        break;
+      if (elect_one()) {
+        if (i >= early) {
+          mbar_arrive_expect_tx(&sm.full[s], Smem::kStageBytes);
+          tma_load_2d(sm.stage[s], &tm_w, &sm.full[s], (kb0 + i) * 128, n0);
+        }
+        tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, t0);
+        mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
+        bulk_load(sm.sa[q], args.sa + (kb0 + i) * args.ld_sa + t0, sa_bytes, &sm.sa_full[q]);
+      }
+      __syncwarp();
+      issued = i + 1;
+    }
+    if (lane == 0 && *abort_flag) {
+      // wait for the copies still in flight, so none lands after teardown
+      const uint32_t first = issued > NST ? issued - NST : 0;
+      for (uint32_t i = first; i < issued; ++i) {
+        mbar_wait_bounded(&sm.full[i % NST], (i / NST) & 1u, nullptr, DEVERR_TIMEOUT_PRODUCER);
+        mbar_wait_bounded(&sm.sa_full[i % Smem::kSaSlots], (i / Smem::kSaSlots) & 1u, nullptr,
+                          DEVERR_TIMEOUT_PRODUCER);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ============================ MMA issuer ==============================
+    pdl_wait();
+    const uint64_t dw0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]));
+    const uint64_t dx0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]) + F_W_BYTES);
+    for (int i = 0; i < nk; ++i) {
+      const int s = i % NST;
+      const uint32_t b = i & 1;
+      if (!warp_wait_bounded(&sm.acc_empty[b], ((i >> 1) & 1) ^ 1u, abort_flag, DEVERR_TIMEOUT_MMA))
+        break;
+      if (!warp_wait_bounded(&sm.full[s], (i / NST) & 1u, abort_flag, DEVERR_TIMEOUT_MMA)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t so = static_cast<uint64_t>(s * (Smem::kStageBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f8(tmem + b * N, dw0 + so + 2 * kk, dx0 + so + 2 * kk, idesc_f8(128, N), kk != 0);
+        tc_commit(&sm.empty[s]);
+        tc_commit(&sm.acc_full[b]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) tc_commit(&sm.drain);
+    __syncwarp();
+    mbar_wait_bounded(&sm.drain, 0u, nullptr, DEVERR_TIMEOUT_MMA);
+    __syncwarp();
+  } else {
+    // ============================ epilogue ================================
+    pdl_wait();
+    const int sp = warp & 3;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
+    const float* sbp = args.sb + static_cast<int64_t>(blockIdx.x) * args.nkb + kb0;
+    float2 acc[N / 2];
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    float sb = nk > 0 ? __ldg(sbp) : 0.f;
+    for (int i = 0; i < nk; ++i) {
+      const int q = i % Smem::kSaSlots;
+      const uint32_t b = i & 1;
+      const float sb_next = i + 1 < nk ? __ldg(sbp + i + 1) : 0.f;
+      if (!warp_wait_bounded(&sm.sa_full[q], (i / Smem::kSaSlots) & 1u, abort_flag,
+                             DEVERR_TIMEOUT_EPILOGUE) ||
+          !warp_wait_bounded(&sm.acc_full[b], (i >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
+        break;
+      tc_fence_after();
+      constexpr int CH = N < 32 ? 16 : 32;
+#pragma unroll
+      for (int c = 0; c < N / CH; ++c) {
+        uint32_t r[CH];
+        if constexpr (CH == 16) tmem_ld_32x32b_x16(taddr + b * N + c * CH, r);
+        else tmem_ld_32x32b_x32(taddr + b * N + c * CH, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < CH / 4; ++j) {
+          const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][c * CH + 4 * j]);
+          float2& a0 = acc[c * CH / 2 + 2 * j];
+          float2& a1 = acc[c * CH / 2 + 2 * j + 1];
+          a0 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
+                          make_float2(s4.x * sb, s4.y * sb), a0);
+          a1 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
+                          make_float2(s4.z * sb, s4.w * sb), a1);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+      sb = sb_next;
+    }
+    // this CTA's sums, [token][channel], over the ring: the last accumulator is
+    // complete, so every tile has arrived and been read
+    if (*abort_flag == 0u) {
+      float* red = reinterpret_cast<float*>(sm.stage[0]) + 32 * sp + lane;
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        red[(2 * j) * 128] = acc[j].x;
+        red[(2 * j + 1) * 128] = acc[j].y;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TCOLS);
+  }
+  __syncwarp();
+  cluster_sync_all();
+  if (*abort_flag == 0u) {
+    // CTA r of the cluster joins tokens r, r + C, ...: the ranks' sums in order
+    const uint32_t red = smem_u32(sm.stage[0]);
+    for (int i = threadIdx.x; i < ((nt - rank + C - 1) / C) * 64; i += F_THREADS) {
+      const int t = rank + (i >> 6) * C, c = 2 * (i & 63);
+      if (n0 + c >= args.d_out) continue;                  // d_out is even
+      float2 v = make_float2(0.f, 0.f);
+      for (int r = 0; r < C; ++r) {
+        const float2 p = ld_cluster_f32x2(mapa_shared(red + 4u * (t * 128 + c), r));
+        v.x += p.x;
+        v.y += p.y;
+      }
+      const int64_t at = (t0 + t) * args.ldy + n0 + c;
+      if constexpr (kF32) {
+        *reinterpret_cast<float2*>(static_cast<float*>(args.Y) + at) = v;
+      } else {
+        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(args.Y) + at) =
+            __floats2bfloat162_rn(v.x, v.y);
+      }
+    }
+  }
+  cluster_sync_all();          // no CTA leaves while another reads its sums
+}
+
+// ---------------------------------------------------------------------------
+// CTA pairs
+// ---------------------------------------------------------------------------
+constexpr int Q_STAGES = 6;
+constexpr int Q_HALF = 128 * 128;                     // own 128 rows of A, and of B
+constexpr int Q_STAGE_BYTES = 2 * Q_HALF;
+constexpr int Q_THREADS = 384;                        // producer, MMA, 2 idle, 8 epilogue warps
+constexpr int Q_EPI_WARPS = 8;
+constexpr int Q_GROUP_M = 16;
+
+struct Fp8PairSmem {
+  uint8_t stage[Q_STAGES][Q_STAGE_BYTES];
+  alignas(1024) uint8_t epi[Q_EPI_WARPS][2][1024];
+  uint64_t full[Q_STAGES];      // leader's counts the bytes of both CTAs
+  uint64_t empty[Q_STAGES];     // both CTAs: MMA commit, multicast
+  uint64_t acc_full[2];         // both CTAs: MMA commit, multicast
+  uint64_t acc_empty[2];        // leader: epilogue warps of both CTAs
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <bool kF32>
+__global__ void __launch_bounds__(Q_THREADS, 1)
+    fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x,
+                         const __grid_constant__ CUtensorMap tm_w,
+                         const __grid_constant__ CUtensorMap tm_y,
+                         const __grid_constant__ Fp8GemmArgs args) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Fp8PairSmem& sm = *reinterpret_cast<Fp8PairSmem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  volatile uint32_t* abort_flag = &sm.abort_flag;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();          // 0 = leader
+  const int pair = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+  const int ntiles = args.tiles_m * args.tiles_n;
+  const int nkb = args.nkb;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Q_STAGES; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 2 * Q_EPI_WARPS);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0u;
+    fence_barrier_init();
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_y);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&sm.tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp < 4) {
+    // the launch's 384 x 168 registers: 128 x 56 here, 256 x 224 for the epilogue
+    setmaxnreg_dec<56>();
+    if (warp == 0) {
+      // ============================ TMA producer (both CTAs) ==============
+      uint32_t issued = 0, it = 0, s = 0, ph = 0;
+      bool ok = true;
+      for (int t = pair; t < ntiles && ok; t += npairs) {
+        int tm, tn;
+        tile_coords<Q_GROUP_M>(t, args.tiles_m, args.tiles_n, tm, tn);
+        const int m_rows = tm * 256 + 128 * static_cast<int>(rank);
+        const int n_rows = tn * 256 + 128 * static_cast<int>(rank);
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          if (it >= Q_STAGES &&
+              !warp_wait_bounded(&sm.empty[s], ph ^ 1u, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            const uint32_t full_leader = mapa_shared(smem_u32(&sm.full[s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Q_STAGE_BYTES);
+            tma_load_2d_pair(sm.stage[s], &tm_x, full_leader, kb * 128, m_rows);
+            tma_load_2d_pair(sm.stage[s] + Q_HALF, &tm_w, full_leader, kb * 128, n_rows);
+          }
+          __syncwarp();
+          issued = it + 1;
+          if (++s == Q_STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (lane == 0 && *abort_flag) {
+        if (rank == 0) {
+          const uint32_t first = issued > Q_STAGES ? issued - Q_STAGES : 0;
+          for (uint32_t i = first; i < issued; ++i)
+            mbar_wait_bounded(&sm.full[i % Q_STAGES], (i / Q_STAGES) & 1u, nullptr,
+                              DEVERR_TIMEOUT_PRODUCER);
+        }
+        spin_ns(50000);            // the peer CTA's copies land on the leader's barriers
+      }
+      __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+      // ============================ MMA issuer (leader) ===================
+      constexpr uint64_t STAGE_DESC = Q_STAGE_BYTES >> 4;
+      constexpr uint32_t ID = idesc_f8(256, 256);
+      const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]));
+      const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]) + Q_HALF);
+      uint32_t s = 0, ph = 0, g = 0;
+      uint64_t soff = 0;
+      bool ok = true;
+      for (int t = pair; t < ntiles && ok; t += npairs) {
+        for (int kb = 0; kb < nkb; ++kb, ++g) {
+          const uint32_t b = g & 1u;
+          if (!warp_wait_bounded(&sm.acc_empty[b], ((g >> 1) & 1u) ^ 1u, abort_flag,
+                                 DEVERR_TIMEOUT_MMA) ||
+              !warp_wait_bounded(&sm.full[s], ph, abort_flag, DEVERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t d = tmem + 256u * b;
+            mma_f8_pair(d, da0 + soff + 0, db0 + soff + 0, ID, 0u);
+            mma_f8_pair(d, da0 + soff + 2, db0 + soff + 2, ID, 1u);
+            mma_f8_pair(d, da0 + soff + 4, db0 + soff + 4, ID, 1u);
+            mma_f8_pair(d, da0 + soff + 6, db0 + soff + 6, ID, 1u);
+            tc_commit_pair_multicast(&sm.empty[s], 0x3);
+            tc_commit_pair_multicast(&sm.acc_full[b], 0x3);
+          }
+          __syncwarp();
+          if (++s == Q_STAGES) {
+            s = 0;
+            ph ^= 1u;
+            soff = 0;
+          } else {
+            soff += STAGE_DESC;
+          }
+        }
+      }
+      if (elect_one()) tc_commit_pair(&sm.drain);
+      __syncwarp();
+      mbar_wait_bounded(&sm.drain, 0u, nullptr, DEVERR_TIMEOUT_MMA);
+      __syncwarp();
+    }
+  } else {
+    // ============================ epilogue (both CTAs) ====================
+    // Each warp owns 32 rows (its lanes) x 128 columns: 128 sums a lane.
+    setmaxnreg_inc<224>();
+    const int ew = warp - 4;
+    const int sp = warp & 3;
+    const int half = ew >> 2;
+    const uint32_t acc_empty_leader = mapa_shared(smem_u32(&sm.acc_empty[0]), 0);
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16) + 128 * half;
+    const uint32_t stg = smem_u32(sm.epi[ew]);
+    uint32_t g = 0, buf = 0;
+    bool ok = true;
+    for (int t = pair; t < ntiles && ok; t += npairs) {
+      int tm, tn;
+      tile_coords<Q_GROUP_M>(t, args.tiles_m, args.tiles_n, tm, tn);
+      const int row0 = tm * 256 + 128 * static_cast<int>(rank) + 32 * sp;
+      const int row = row0 + lane;
+      const int nblk = tn * 2 + half;
+      const bool rin = row < args.T, nin = nblk * 128 < args.d_out;
+      const float* sap = args.sa + row;
+      const float* sbp = args.sb + static_cast<int64_t>(nblk) * nkb;
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+      float sa = rin ? __ldg(sap) : 0.f;
+      float sb = nin ? __ldg(sbp) : 0.f;
+      for (int kb = 0; kb < nkb; ++kb, ++g) {
+        const uint32_t b = g & 1u;
+        const float m = sa * sb;
+        const bool more = kb + 1 < nkb;
+        sa = rin && more ? __ldg(sap + (kb + 1) * args.ld_sa) : 0.f;
+        sb = nin && more ? __ldg(sbp + kb + 1) : 0.f;
+        if (!warp_wait_bounded(&sm.acc_full[b], (g >> 1) & 1u, abort_flag,
+                               DEVERR_TIMEOUT_EPILOGUE)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float2 m2 = make_float2(m, m);
+        const uint32_t ta = taddr + 256u * b;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(ta + 32 * c, r);
+          tmem_ld_wait();
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8u * b);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[16 * c + j] = __ffma2_rn(
+                make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), m2,
+                acc[16 * c + j]);
+        }
+      }
+      if (!ok) break;
+      // Y through staging blocks of 16 rows x 64 bytes (64-byte swizzle), as
+      // the dual-branch GEMM stores it: 32 bf16 or 16 f32 columns a block,
+      // two blocks in turn
+      constexpr int CB = kF32 ? 16 : 32;                   // columns per block
+#pragma unroll
+      for (int c = 0; c < 128 / CB; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if constexpr (kF32) {
+            const float2 v = acc[8 * c + (j >> 1)];
+            p[j] = __float_as_uint((j & 1) ? v.y : v.x);
+          } else {
+            const float2 v = acc[16 * c + j];
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v.x, v.y);
+            p[j] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+        }
+        const int col = tn * 256 + 128 * half + CB * c;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t blk = stg + 1024u * buf;
+          buf ^= 1u;
+          // the store before the last one has read its block
+          if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+          if ((lane >> 4) == hh) {
+            const uint32_t rl = static_cast<uint32_t>(lane & 15);
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q)
+              st_shared_v4(blk + rl * 64u + 16u * (q ^ ((rl >> 1) & 3u)), p[4 * q], p[4 * q + 1],
+                           p[4 * q + 2], p[4 * q + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one()) {
+            tma_store_2d(&tm_y, blk, col, row0 + 16 * hh);
+            bulk_commit_group();
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (elect_one()) bulk_wait_group0();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_sync_all();          // the pair's MMAs, copies and remote arrivals are done
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+template <int N>
+static cudaError_t few_attr() {
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  const int bytes = static_cast<int>(sizeof(FewSmem<N>) + 1024);
+  e = cudaFuncSetAttribute(fp8_gemm_few_kernel<N, false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fp8_gemm_few_kernel<N, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
+  return e;
+}
+
+static int fp8_pair_capacity() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cached[dev] > 0) return cached[dev];
+  const size_t smem = sizeof(Fp8PairSmem) + 1024;
+  if (cudaFuncSetAttribute(fp8_gemm_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess ||
+      cudaFuncSetAttribute(fp8_gemm_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * 148, 1, 1);
+  cfg.blockDim = dim3(Q_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0, n2 = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_pair_kernel<false>, &cfg) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n2, fp8_gemm_pair_kernel<true>, &cfg) != cudaSuccess)
+    return 0;
+  cached[dev] = n < n2 ? n : n2;
+  return cached[dev];
+}
+
+// Token counts up to this take the few-token kernel.
+constexpr int64_t kFp8FewMaxT = 512;
+
+cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int64_t T, int64_t d_in,
+                          int64_t d_out, const uint8_t* wq, const float* wscale, void* Y, int64_t ldy,
+                          bool f32, bool early_weights, Fp8GemmPlan* p) {
+  memset(p, 0, sizeof(*p));
+  p->empty = T == 0;
+  if (p->empty) return cudaSuccess;
+  p->f32 = f32;
+  Fp8GemmArgs& a = p->a;
+  a.sa = sa;
+  a.sb = wscale;
+  a.Y = Y;
+  a.ld_sa = ld_sa;
+  a.ldy = ldy;
+  a.T = static_cast<int>(T);
+  a.d_out = static_cast<int>(d_out);
+  a.nkb = static_cast<int>((d_in + kFp8Block - 1) / kFp8Block);
+  a.early_weights = early_weights ? 1 : 0;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (T <= kFp8FewMaxT) {
+    const int N = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    cudaError_t e = N == 16 ? few_attr<16>() : N == 32 ? few_attr<32>() : N == 64 ? few_attr<64>() : few_attr<128>();
+    if (e != cudaSuccess) return e;
+    p->few = N;
+    p->smem = (N == 16 ? sizeof(FewSmem<16>) : N == 32 ? sizeof(FewSmem<32>)
+               : N == 64 ? sizeof(FewSmem<64>) : sizeof(FewSmem<128>)) + 1024;
+    const int tn = static_cast<int>((d_out + 127) / 128), tt = static_cast<int>((T + N - 1) / N);
+    // K is split while the tiles leave SMs without work (148 SMs, two CTAs each)
+    int C = 1;
+    while (C < 8 && 2 * C <= a.nkb && static_cast<int64_t>(tn) * tt * C < 120) C *= 2;
+    p->cluster = C;
+    p->grid = dim3(tn, tt, C);
+    if (!make_tmap(&p->tm_w, wq, u8, 1, d_in, d_out, d_in, 128) ||
+        !make_tmap(&p->tm_x, aq, u8, 1, d_in, T, d_in, N))
+      return cudaErrorInvalidValue;
+    return cudaSuccess;
+  }
+  const int cap = fp8_pair_capacity();
+  if (cap <= 0) return cudaErrorInvalidConfiguration;
+  a.tiles_m = static_cast<int>((T + 255) / 256);
+  a.tiles_n = static_cast<int>((d_out + 255) / 256);
+  const int64_t ntiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+  if (ntiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  p->grid = dim3(static_cast<unsigned>(2 * (ntiles < cap ? ntiles : cap)));
+  p->smem = sizeof(Fp8PairSmem) + 1024;
+  const int eb = f32 ? 4 : 2;
+  if (!make_tmap(&p->tm_x, aq, u8, 1, d_in, T, d_in, 128) ||
+      !make_tmap(&p->tm_w, wq, u8, 1, d_in, d_out, d_in, 128) ||
+      !make_tmap(&p->tm_y, Y, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                 eb, d_out, T, static_cast<uint64_t>(ldy) * eb, 16, 64 / eb, false,
+                 CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+cudaError_t run_fp8_gemm(const Fp8GemmPlan& p, cudaStream_t stream) {
+  if (p.empty) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = p.grid;
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + static_cast<unsigned>(pdl_attrs(&attr[1]));
+  if (p.few) {
+    cfg.blockDim = dim3(F_THREADS, 1, 1);
+    attr[0].val.clusterDim.z = static_cast<unsigned>(p.cluster);
+    void (*k)(CUtensorMap, CUtensorMap, Fp8GemmArgs) = nullptr;
+    if (p.few == 16) k = p.f32 ? fp8_gemm_few_kernel<16, true> : fp8_gemm_few_kernel<16, false>;
+    else if (p.few == 32) k = p.f32 ? fp8_gemm_few_kernel<32, true> : fp8_gemm_few_kernel<32, false>;
+    else if (p.few == 64) k = p.f32 ? fp8_gemm_few_kernel<64, true> : fp8_gemm_few_kernel<64, false>;
+    else k = p.f32 ? fp8_gemm_few_kernel<128, true> : fp8_gemm_few_kernel<128, false>;
+    return cudaLaunchKernelEx(&cfg, k, p.tm_w, p.tm_x, p.a);
+  }
+  cfg.blockDim = dim3(Q_THREADS, 1, 1);
+  attr[0].val.clusterDim.x = 2;
+  return cudaLaunchKernelEx(&cfg, p.f32 ? fp8_gemm_pair_kernel<true> : fp8_gemm_pair_kernel<false>,
+                            p.tm_x, p.tm_w, p.tm_y, p.a);
+}
+
+}  // namespace w4a4

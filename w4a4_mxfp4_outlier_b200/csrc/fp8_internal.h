@@ -1,0 +1,38 @@
+// Internal declarations of the 8-bit floating point operators.
+#pragma once
+
+#include "w4a4_internal.h"
+
+namespace w4a4 {
+
+cudaError_t launch_fp8_quant_act(const void* X, int64_t T, int64_t d, int64_t ldx, uint8_t* q,
+                                 float* scale, int64_t ld_scale, cudaStream_t stream);
+cudaError_t launch_fp8_pack_weight(const void* W, int64_t ldw, int64_t rows, int64_t cols,
+                                   int64_t experts, uint8_t* q, float* scale, cudaStream_t stream);
+
+struct Fp8GemmArgs {
+  const float* sa;          // [nkb][ld_sa]
+  const float* sb;          // [ceil(d_out / 128)][nkb]
+  void* Y;
+  int64_t ld_sa, ldy;
+  int T, d_out, nkb;
+  int tiles_m, tiles_n;     // pair kernel
+  int early_weights;        // weights may be read before the previous kernel has ended
+};
+
+// plan: tensor maps, tile choice (host only); run: the launch.
+struct Fp8GemmPlan {
+  CUtensorMap tm_x, tm_w, tm_y;
+  Fp8GemmArgs a;
+  dim3 grid;
+  size_t smem;
+  int few;                  // 0: pair kernel; else tokens per tile of the few-token kernel
+  int cluster;
+  bool f32, empty;
+};
+cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int64_t T, int64_t d_in,
+                          int64_t d_out, const uint8_t* wq, const float* wscale, void* Y, int64_t ldy,
+                          bool f32, bool early_weights, Fp8GemmPlan* p);
+cudaError_t run_fp8_gemm(const Fp8GemmPlan& p, cudaStream_t stream);
+
+}  // namespace w4a4

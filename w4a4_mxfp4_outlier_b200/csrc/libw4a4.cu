@@ -11,3 +11,6 @@
 #include "checkpoint.cu"
 #include "metrics.cu"
 #include "ffn.cu"
+#include "fp8_quant.cu"
+#include "fp8_gemm.cu"
+#include "fp8_api.cu"

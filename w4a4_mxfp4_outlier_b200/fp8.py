@@ -1,0 +1,199 @@
+"""8-bit floating point (e4m3) linear layer with one scale per block of 128.
+
+For projections that do not stand 4 bits, or whose weights come from a
+checkpoint in this format: activations have one float32 scale per token and
+128 columns, weights one per 128 x 128 tile, and an e4m3 code c of a block with
+scale s stands for c * s.
+
+    w = pack_weight(W)                    # or Fp8Weight(q, scale) from a checkpoint
+    ws = torch.empty(workspace_size(T, w), dtype=torch.uint8, device="cuda")
+    linear(X, w, ws, Y)                   # quant_act, then gemm
+
+quant_act and pack_weight choose the smallest power of two s with
+max|x| <= 448 s; the product takes any float32 scales.  Every call checks its
+tensors and the status the library returns, runs on the tensors' device and on
+the given stream (default: that device's current stream), and allocates
+nothing unless it says so.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass, field
+
+import torch
+
+from . import (ERR_INVALID_ARG, W4A4Error, _check, _i64, _rows_bf16, _sig, _st, _vp)
+
+BLOCK = 128
+
+
+class Fp8WeightC(ctypes.Structure):
+    _fields_ = [("d_in", _i64), ("d_out", _i64), ("experts", _i64), ("q", _vp), ("scale", _vp)]
+
+
+_PW = ctypes.POINTER(Fp8WeightC)
+_quant_act = _sig("w4a4_fp8_quant_act", _st, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp)
+_pack_weight = _sig("w4a4_fp8_pack_weight", _st, _vp, _i64, _PW, _vp)
+_gemm = _sig("w4a4_fp8_gemm", _st, _vp, _vp, _i64, _i64, _PW, _vp, _i64, ctypes.c_int, _vp)
+_workspace_size = _sig("w4a4_fp8_workspace_size", _st, _i64, _i64, ctypes.POINTER(ctypes.c_size_t))
+_linear = _sig("w4a4_fp8_linear", _st, _vp, _i64, _i64, _PW, _vp, ctypes.c_size_t, _vp, _i64,
+               ctypes.c_int, _vp)
+
+
+def blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _run(device: torch.device, stream, what: str, fn, *args):
+    """fn(*args, stream) with `device` current; raises on a non-OK status."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, s), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, s), what)
+
+
+def _dense(t: torch.Tensor, dtypes, shape, device, what: str):
+    """A dense tensor of one of `dtypes`, `shape` and `device`."""
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or \
+            not t.is_cuda or (device is not None and t.device != device):
+        raise W4A4Error(ERR_INVALID_ARG,
+                        f"{what}: needs a dense {'/'.join(str(d) for d in dtypes)} CUDA tensor of "
+                        f"shape {tuple(shape)}{' on ' + str(device) if device is not None else ''} "
+                        f"(got {t.dtype}, {tuple(t.shape)}, strides {tuple(t.stride())}, {t.device})")
+
+
+def _bytes(t: torch.Tensor, device, what: str):
+    """A workspace: any dense CUDA tensor on `device`."""
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise W4A4Error(ERR_INVALID_ARG, f"{what}: the workspace must be a dense tensor on {device} "
+                                         f"(got strides {tuple(t.stride())}, {t.device})")
+
+
+def _rows_out(Y: torch.Tensor, rows: int, cols: int, device, what: str) -> int:
+    """An output [rows, cols], bf16 or float32, unit column stride; its y_f32."""
+    if Y.dtype not in (torch.bfloat16, torch.float32) or tuple(Y.shape) != (rows, cols) or \
+            Y.device != device or (cols > 1 and Y.stride(1) != 1):
+        raise W4A4Error(ERR_INVALID_ARG,
+                        f"{what}: Y must be bfloat16 or float32 [{rows}, {cols}] on {device} with unit "
+                        f"column stride (got {Y.dtype}, {tuple(Y.shape)}, strides {tuple(Y.stride())}, "
+                        f"{Y.device})")
+    return int(Y.dtype == torch.float32)
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor; of one with at most one row, its dense row stride."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1] + 7 & ~7, 8)
+
+
+_F8 = (torch.uint8, torch.float8_e4m3fn)
+
+
+@dataclass
+class Fp8Weight:
+    """e4m3 codes [d_out, d_in] with float32 scales [ceil(d_out/128),
+    ceil(d_in/128)], or a stack of them with a leading dimension."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    c: Fp8WeightC = field(init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        if self.q.dim() not in (2, 3):
+            raise W4A4Error(ERR_INVALID_ARG, f"Fp8Weight: q has {self.q.dim()} dimensions, not 2 or 3")
+        lead, (d_out, d_in) = tuple(self.q.shape[:-2]), self.q.shape[-2:]
+        _dense(self.q, _F8, self.q.shape, None, "Fp8Weight q")
+        _dense(self.scale, (torch.float32,), lead + (blocks(d_out), blocks(d_in)), self.q.device,
+               "Fp8Weight scale")
+        self.c = Fp8WeightC(d_in, d_out, lead[0] if lead else 1, self.q.data_ptr(),
+                            self.scale.data_ptr())
+
+    @property
+    def d_in(self) -> int:
+        return self.c.d_in
+
+    @property
+    def d_out(self) -> int:
+        return self.c.d_out
+
+    @property
+    def experts(self) -> int:
+        return self.c.experts
+
+    @property
+    def device(self) -> torch.device:
+        return self.q.device
+
+
+@dataclass
+class Fp8Act:
+    """Quantised activations: q uint8 [T, d], scale float32 [ceil(d/128), ld]
+    (token t and block b at [b, t]; ld is T rounded up to 4)."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+def alloc_act(T: int, d: int, device="cuda") -> Fp8Act:
+    return Fp8Act(torch.empty((T, d), dtype=torch.uint8, device=device),
+                  torch.empty((blocks(d), max(4, (T + 3) // 4 * 4)), dtype=torch.float32, device=device))
+
+
+def quant_act(X: torch.Tensor, out: Fp8Act, stream=None) -> Fp8Act:
+    T, d = X.shape if X.dim() == 2 else (-1, -1)
+    _rows_bf16(X, "fp8.quant_act")
+    _dense(out.q, _F8, (T, d), X.device, "fp8.quant_act q")
+    _dense(out.scale, (torch.float32,), (blocks(d), out.scale.shape[-1]), X.device,
+           "fp8.quant_act scale")
+    _run(X.device, stream, "fp8.quant_act", _quant_act, X.data_ptr(), T, d, _ld(X), out.q.data_ptr(),
+         out.scale.data_ptr(), out.scale.shape[1])
+    return out
+
+
+def pack_weight(W: torch.Tensor, stream=None) -> Fp8Weight:
+    """Quantises W, bf16 [d_out, d_in] or dense [experts, d_out, d_in]; allocates the result."""
+    if W.dim() == 3:
+        _dense(W, (torch.bfloat16,), W.shape, None, "fp8.pack_weight")
+        ldw = W.shape[2]
+    else:
+        _rows_bf16(W, "fp8.pack_weight")
+        ldw = _ld(W)
+    d_out, d_in = W.shape[-2:]
+    w = Fp8Weight(torch.empty(W.shape, dtype=torch.uint8, device=W.device),
+                  torch.empty(tuple(W.shape[:-2]) + (blocks(d_out), blocks(d_in)), dtype=torch.float32,
+                              device=W.device))
+    _run(W.device, stream, "fp8.pack_weight", _pack_weight, W.data_ptr(), ldw, ctypes.byref(w.c))
+    return w
+
+
+def gemm(act: Fp8Act, w: Fp8Weight, Y: torch.Tensor, stream=None) -> torch.Tensor:
+    """Y = act @ w^T, bf16 or float32 by Y's type."""
+    T = act.q.shape[0]
+    _dense(act.q, _F8, (T, w.d_in), w.device, "fp8.gemm q")
+    _dense(act.scale, (torch.float32,), (blocks(w.d_in), act.scale.shape[-1]), w.device,
+           "fp8.gemm scale")
+    f32 = _rows_out(Y, T, w.d_out, w.device, "fp8.gemm")
+    _run(w.device, stream, "fp8.gemm", _gemm, act.q.data_ptr(), act.scale.data_ptr(),
+         act.scale.shape[1], T, ctypes.byref(w.c), Y.data_ptr(), _ld(Y), f32)
+    return Y
+
+
+def workspace_size(T: int, w: Fp8Weight) -> int:
+    n = ctypes.c_size_t()
+    _check(_workspace_size(T, w.d_in, ctypes.byref(n)), "fp8.workspace_size")
+    return n.value
+
+
+def linear(X: torch.Tensor, w: Fp8Weight, workspace: torch.Tensor, Y: torch.Tensor,
+           stream=None) -> torch.Tensor:
+    """Y = quant_act(X) @ w^T, bf16 or float32 by Y's type."""
+    _rows_bf16(X, "fp8.linear", w.device)
+    T = X.shape[0]
+    if X.shape[1] != w.d_in:
+        raise W4A4Error(ERR_INVALID_ARG, f"fp8.linear: X has {X.shape[1]} columns, w {w.d_in}")
+    f32 = _rows_out(Y, T, w.d_out, w.device, "fp8.linear")
+    _bytes(workspace, w.device, "fp8.linear")
+    _run(w.device, stream, "fp8.linear", _linear, X.data_ptr(), T, _ld(X), ctypes.byref(w.c),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size(), Y.data_ptr(), _ld(Y), f32)
+    return Y
