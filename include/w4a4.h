@@ -389,6 +389,52 @@ w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp
                             void* workspace, size_t ws_bytes, void* Y, int64_t ldy, int y_f32,
                             void* stream);
 
+/* ------------------------------------------------------------------------
+ * A mixture-of-experts layer for a few tokens (T <= 64), whole, in two
+ * kernels: router, selection, the chosen experts' two projections and the
+ * weighted sum.
+ *   l[t, e] = sum_j x[t, j] router[e, j]              (float32)
+ *   E_t     = the top_k experts of largest l, equal ones by lower index, NaN last
+ *   w[t, e] = exp(l[t, e]) / sum exp(l[t, .]), the sum over E_t (renorm != 0)
+ *             or over all experts
+ *   h       = silu(gate_e x) * (up_e x)   (act = W4A4_MOE_SILU_GATED), or
+ *             gelu(up_e x), tanh form     (act = W4A4_MOE_GELU; gate unused)
+ *   y[t]    = sum over E_t of w[t, e] * (down_e h), in the order of selection
+ * x is quantised as by w4a4_fp8_quant_act, h (float32) by the same rule, and
+ * the products are those of w4a4_fp8_gemm; h is not rounded in between.  K may
+ * be split into ranges whose float32 sums are added in order, by a rule on the
+ * sizes, the number of experts chosen and the device's SM count; results do
+ * not depend on timing.
+ * A token whose x holds an infinity or a NaN gets NaN in all of y (and any
+ * valid expert indexes); other tokens are not affected.
+ * ------------------------------------------------------------------------ */
+typedef enum w4a4_moe_act { W4A4_MOE_GELU = 0, W4A4_MOE_SILU_GATED = 1 } w4a4_moe_act;
+
+typedef struct w4a4_fp8_experts {
+  int64_t top_k;
+  int32_t act;             /* w4a4_moe_act */
+  int32_t renorm;
+  const void* router;      /* bf16 [experts, d], dense */
+  w4a4_fp8_weight gate;    /* experts x [d_ff, d]; all zero with W4A4_MOE_GELU */
+  w4a4_fp8_weight up;      /* experts x [d_ff, d] */
+  w4a4_fp8_weight down;    /* experts x [d, d_ff] */
+} w4a4_fp8_experts;
+
+/* Bytes of device workspace w4a4_fp8_moe needs for T tokens. */
+w4a4_status w4a4_fp8_moe_workspace_size(const w4a4_fp8_experts* m, int64_t T, size_t* bytes);
+
+/* The layer.  X: bf16 [T, d], row stride ldx; Y: bf16 [T, d] or, with
+ * y_f32 != 0, float32, row stride ldy.  ids (int32 [T, top_k], the chosen
+ * experts in order of selection) and weights (float32 [T, top_k], their w) are
+ * written unless NULL.  Limits: T <= 64, experts <= 512, top_k <= 16 and <=
+ * experts, d and d_ff multiples of 16 and at most 65535, ldx and ldy multiples
+ * of 8, pointers 16-byte aligned (ids, weights and scales 4); beyond them
+ * UNSUPPORTED_SHAPE (top_k < 1 or > experts: INVALID_ARG).  Calls that may run
+ * at the same time need workspaces of their own. */
+w4a4_status w4a4_fp8_moe(const void* X, int64_t T, int64_t ldx, const w4a4_fp8_experts* m,
+                         void* workspace, size_t ws_bytes, void* Y, int64_t ldy, int y_f32,
+                         int32_t* ids, float* weights, void* stream);
+
 /* Size of the fixed device scratch array behind w4a4_linear_noalloc. */
 #define W4A4_NOALLOC_SCRATCH_BYTES ((size_t)32 << 20)
 

@@ -110,7 +110,7 @@ EXPORTED = [
     "w4a4_error_sums", "w4a4_gelu_bf16", "w4a4_ffn_link", "w4a4_pack_weight_rows", "w4a4_permute_packed_rows",
     "w4a4_gemm_dual_act", "w4a4_test_fault",
     "w4a4_fp8_quant_act", "w4a4_fp8_pack_weight", "w4a4_fp8_gemm", "w4a4_fp8_workspace_size",
-    "w4a4_fp8_linear",
+    "w4a4_fp8_linear", "w4a4_fp8_moe_workspace_size", "w4a4_fp8_moe",
 ]
 
 

@@ -62,6 +62,27 @@ static Fp8Workspace fp8_workspace(int64_t T, int64_t d_in) {
   return w;
 }
 
+static w4a4_status moe_check(const w4a4_fp8_experts* m, int64_t T) {
+  if (m == nullptr || T < 0) return W4A4_ERR_INVALID_ARG;
+  if (m->act != W4A4_MOE_GELU && m->act != W4A4_MOE_SILU_GATED) return W4A4_ERR_INVALID_ARG;
+  w4a4_status st = fp8_check_weight(&m->up);
+  if (st != W4A4_OK) return st;
+  st = fp8_check_weight(&m->down);
+  if (st != W4A4_OK) return st;
+  const int64_t d = m->up.d_in, ff = m->up.d_out, E = m->up.experts;
+  if (m->down.d_in != ff || m->down.d_out != d || m->down.experts != E) return W4A4_ERR_INVALID_ARG;
+  if (m->act == W4A4_MOE_SILU_GATED) {
+    st = fp8_check_weight(&m->gate);
+    if (st != W4A4_OK) return st;
+    if (m->gate.d_in != d || m->gate.d_out != ff || m->gate.experts != E) return W4A4_ERR_INVALID_ARG;
+  }
+  if (m->router == nullptr || m->top_k < 1 || m->top_k > E) return W4A4_ERR_INVALID_ARG;
+  if (T > kMoeMaxT || E > kMoeMaxE || m->top_k > kMoeMaxK || ff > 65535 || d > 65535 ||
+      !aligned16(m->router))
+    return W4A4_ERR_UNSUPPORTED_SHAPE;
+  return W4A4_OK;
+}
+
 }  // namespace w4a4
 
 using namespace w4a4;
@@ -131,6 +152,74 @@ w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   e = launch_fp8_quant_act(X, T, w->d_in, ldx, q, scale, ws.ld_scale, s);
   if (e == cudaSuccess) e = run_fp8_gemm(p, s);
+  return from_cuda(e);
+}
+
+w4a4_status w4a4_fp8_moe_workspace_size(const w4a4_fp8_experts* m, int64_t T, size_t* bytes) {
+  if (bytes == nullptr) return W4A4_ERR_INVALID_ARG;
+  const w4a4_status st = moe_check(m, T);
+  if (st != W4A4_OK) return st;
+  *bytes = moe_layout(T, m->up.d_in, m->up.d_out, m->up.experts, m->top_k,
+                      m->act == W4A4_MOE_SILU_GATED).total;
+  return W4A4_OK;
+}
+
+w4a4_status w4a4_fp8_moe(const void* X, int64_t T, int64_t ldx, const w4a4_fp8_experts* m,
+                         void* workspace, size_t ws_bytes, void* Y, int64_t ldy, int y_f32,
+                         int32_t* ids, float* weights, void* stream) {
+  const w4a4_status st = moe_check(m, T);
+  if (st != W4A4_OK) return st;
+  const int64_t d = m->up.d_in, ff = m->up.d_out, E = m->up.experts;
+  const bool gated = m->act == W4A4_MOE_SILU_GATED;
+  if (ldx < d || ldy < d) return W4A4_ERR_INVALID_ARG;
+  if (ldx % 8 != 0 || ldy % 8 != 0) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return W4A4_OK;
+  const MoeLayout l = moe_layout(T, d, ff, E, m->top_k, gated);
+  if (X == nullptr || Y == nullptr || workspace == nullptr || ws_bytes < l.total)
+    return W4A4_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(ids) & 3u) != 0 || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0)
+    return W4A4_ERR_UNSUPPORTED_SHAPE;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  MoeArgs a = {};
+  a.X = static_cast<const __nv_bfloat16*>(X);
+  a.router = static_cast<const __nv_bfloat16*>(m->router);
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.Y = Y;
+  a.ids_out = ids;
+  a.wts_out = weights;
+  a.gate_s = m->gate.scale;
+  a.up_s = m->up.scale;
+  a.down_s = m->down.scale;
+  a.xq = base + l.xq;
+  a.xs = reinterpret_cast<float*>(base + l.xs);
+  a.ids = reinterpret_cast<int32_t*>(base + l.ids);
+  a.wts = reinterpret_cast<float*>(base + l.wts);
+  a.hq = base + l.hq;
+  a.hs = reinterpret_cast<float*>(base + l.hs);
+  a.part_up = reinterpret_cast<float*>(base + l.part_up);
+  a.part_dn = reinterpret_cast<float*>(base + l.part_dn);
+  a.counters = reinterpret_cast<int32_t*>(base + l.counters);
+  a.up_done = a.counters + l.up_done;
+  a.ready = a.counters + l.ready;
+  a.dn_done = a.counters + l.dn_done;
+  a.ticket = a.counters + l.ticket;
+  a.ld_x = l.ld_x;
+  a.pairs = l.pairs;
+  a.T = static_cast<int>(T);
+  a.d = static_cast<int>(d);
+  a.ff = static_cast<int>(ff);
+  a.E = static_cast<int>(E);
+  a.top_k = static_cast<int>(m->top_k);
+  a.renorm = m->renorm != 0;
+  a.y_f32 = y_f32 != 0;
+  a.ncounters = static_cast<int>(l.ncounters);
+  a.most_up = l.most_up;
+  a.most_dn = l.most_dn;
+  MoePlan p;
+  cudaError_t e = plan_moe(a, E, m->gate.q, m->up.q, m->down.q, gated, &p);
+  if (e == cudaSuccess) e = run_moe(p, static_cast<cudaStream_t>(stream));
   return from_cuda(e);
 }
 

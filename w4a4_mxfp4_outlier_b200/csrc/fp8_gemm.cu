@@ -181,11 +181,11 @@ __global__ void __launch_bounds__(F_THREADS, 2)
     float2 acc[N / 2];
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-    float sb = nk > 0 ? __ldg(sbp) : 0.f;
+    float sb = nk > 0 ? *sbp : 0.f;
     for (int i = 0; i < nk; ++i) {
       const int q = i % Smem::kSaSlots;
       const uint32_t b = i & 1;
-      const float sb_next = i + 1 < nk ? __ldg(sbp + i + 1) : 0.f;
+      const float sb_next = i + 1 < nk ? sbp[i + 1] : 0.f;
       if (!warp_wait_bounded(&sm.sa_full[q], (i / Smem::kSaSlots) & 1u, abort_flag,
                              DEVERR_TIMEOUT_EPILOGUE) ||
           !warp_wait_bounded(&sm.acc_full[b], (i >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
@@ -445,14 +445,14 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      float sa = rin ? __ldg(sap) : 0.f;
-      float sb = nin ? __ldg(sbp) : 0.f;
+      float sa = rin ? *sap : 0.f;
+      float sb = nin ? *sbp : 0.f;
       for (int kb = 0; kb < nkb; ++kb, ++g) {
         const uint32_t b = g & 1u;
         const float m = sa * sb;
         const bool more = kb + 1 < nkb;
-        sa = rin && more ? __ldg(sap + (kb + 1) * args.ld_sa) : 0.f;
-        sb = nin && more ? __ldg(sbp + kb + 1) : 0.f;
+        sa = rin && more ? sap[(kb + 1) * args.ld_sa] : 0.f;
+        sb = nin && more ? sbp[kb + 1] : 0.f;
         if (!warp_wait_bounded(&sm.acc_full[b], (g >> 1) & 1u, abort_flag,
                                DEVERR_TIMEOUT_EPILOGUE)) {
           ok = false;

@@ -35,4 +35,43 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
                           bool f32, bool early_weights, Fp8GemmPlan* p);
 cudaError_t run_fp8_gemm(const Fp8GemmPlan& p, cudaStream_t stream);
 
+// The expert layer.  Pairs are (token, chosen expert), in rows sorted by expert.
+struct MoeArgs {
+  const __nv_bfloat16* X;
+  const __nv_bfloat16* router;      // [E, d]
+  int64_t ldx, ldy;
+  void* Y;
+  int32_t* ids_out;                 // optional, the caller's
+  float* wts_out;
+  const float *gate_s, *up_s, *down_s;
+  // workspace
+  uint8_t* xq;                      // [T, d]
+  float* xs;                        // [blocks of d][ld_x]
+  int32_t* ids;                     // [T, top_k]
+  float* wts;
+  uint8_t* hq;                      // [pairs, ff]
+  float* hs;                        // [blocks of ff][pairs]
+  float* part_up;                   // [split][pairs][gate, up][ff]
+  float* part_dn;                   // [split][pairs][d]
+  int32_t* counters;                // all of the following, zeroed by the router
+  int32_t *up_done, *ready, *dn_done, *ticket;
+  int64_t ld_x, pairs;
+  int T, d, ff, E, top_k, renorm, y_f32, ncounters, most_up, most_dn;
+};
+struct MoeLayout {
+  int64_t pairs, ld_x, up_done, ready, dn_done, ticket, ncounters;
+  int most_up, most_dn;
+  size_t xq, xs, ids, wts, hq, hs, part_up, part_dn, counters, total;
+};
+MoeLayout moe_layout(int64_t T, int64_t d, int64_t ff, int64_t E, int64_t top_k, bool gated);
+struct MoePlan {
+  CUtensorMap tm_gate, tm_up, tm_down, tm_xq, tm_hq;
+  MoeArgs a;
+  int n, ctas;
+  bool gated;
+};
+cudaError_t plan_moe(const MoeArgs& a, int64_t E, const uint8_t* gate, const uint8_t* up,
+                     const uint8_t* down, bool gated, MoePlan* p);
+cudaError_t run_moe(const MoePlan& p, cudaStream_t stream);
+
 }  // namespace w4a4

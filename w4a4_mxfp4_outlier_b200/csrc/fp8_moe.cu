@@ -1,0 +1,888 @@
+// A whole mixture-of-experts layer for a few tokens (T <= 64) in two kernels:
+//
+//   l[t, e] = sum_j x[t, j] r[e, j];  E_t = the top_k experts of largest l
+//   w[t, e] = exp(l[t, e]) / sum exp(l[t, .])  over E_t (renorm) or all experts
+//   h[t, e] = silu(G_e x_t) * (U_e x_t)   or   gelu(U_e x_t)
+//   y[t]    = sum_{e in E_t} w[t, e] D_e h[t, e]
+//
+// with x and h quantised to e4m3 per token and 128 columns, G, U, D in e4m3
+// with one float32 scale per 128 x 128 tile, sums in float32.
+//
+// With few tokens the layer is the reading of the chosen experts' weights.
+//  * moe_route_kernel: router logits, selection, quantisation of x.
+//  * moe_experts_kernel: persistent.  All CTAs take work units from one counter:
+//    first the units of the up projections, then those of the down
+//    projections; a unit is two tiles of 128 weight rows over a range of K.
+//    Each unit's float32 sums go to the workspace (a few columns: little beside
+//    the weights) and the last unit of a block to arrive finishes it in a fixed
+//    order, so results do not depend on timing: for an up block the activation
+//    and the e4m3 codes of h, for 256 columns of y the weighted sum over
+//    experts.  The weight tiles of the following units, those of down units
+//    included, are fetched while h is still being made, so the memory pipe does
+//    not drain between the two projections.
+//    A unit of the down projection waits until its expert's h is complete.
+//    All up units were taken, by running CTAs that wait for nothing, before the
+//    first down unit is: the wait ends however few CTAs of the grid run at once.
+#include <cuda.h>
+
+#include "fp8_device.cuh"
+#include "fp8_internal.h"
+
+namespace w4a4 {
+
+constexpr int kMoeMaxT = 64;
+constexpr int kMoeMaxE = 512;
+constexpr int kMoeMaxK = 16;
+constexpr int kMoeMaxSplit = 8;
+
+// ---------------------------------------------------------------------------
+// Router
+// ---------------------------------------------------------------------------
+constexpr int R_CTAS = 8;          // cluster: the experts are split over its CTAs
+constexpr int R_THREADS = 256;
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+  float s = bf16_lo_to_f32(a.x) * bf16_lo_to_f32(b.x);
+  s = fmaf(bf16_hi_to_f32(a.x), bf16_hi_to_f32(b.x), s);
+  s = fmaf(bf16_lo_to_f32(a.y), bf16_lo_to_f32(b.y), s);
+  s = fmaf(bf16_hi_to_f32(a.y), bf16_hi_to_f32(b.y), s);
+  s = fmaf(bf16_lo_to_f32(a.z), bf16_lo_to_f32(b.z), s);
+  s = fmaf(bf16_hi_to_f32(a.z), bf16_hi_to_f32(b.z), s);
+  s = fmaf(bf16_lo_to_f32(a.w), bf16_lo_to_f32(b.w), s);
+  s = fmaf(bf16_hi_to_f32(a.w), bf16_hi_to_f32(b.w), s);
+  return s;
+}
+
+// One cluster per TG tokens.  Each warp takes two experts at a time over the
+// whole width (the lanes split it, 16 bytes each); the logits of token i go to
+// the shared memory of the cluster's CTA i, whose first warp selects.
+template <int TG>
+__global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_constant__ MoeArgs a) {
+  __shared__ float logits[kMoeMaxE];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int t0 = static_cast<int>(blockIdx.x / R_CTAS) * TG;
+  const int nt = a.T - t0 < TG ? a.T - t0 : TG;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int i = blockIdx.x * R_THREADS + threadIdx.x; i < a.ncounters; i += gridDim.x * R_THREADS)
+    a.counters[i] = 0;
+  cluster_sync_all();          // the other CTAs' shared memory exists
+
+  const int epc = (a.E + R_CTAS - 1) / R_CTAS;
+  const int e_end = (rank + 1) * epc < a.E ? (rank + 1) * epc : a.E;
+  for (int e0 = rank * epc + 2 * warp; e0 < e_end; e0 += 2 * (R_THREADS / 32)) {
+    const bool two = e0 + 1 < e_end;
+    const __nv_bfloat16* r0 = a.router + static_cast<int64_t>(e0) * a.d;
+    const __nv_bfloat16* r1 = two ? r0 + a.d : r0;
+    float acc[2][TG];
+#pragma unroll
+    for (int i = 0; i < TG; ++i) acc[0][i] = acc[1][i] = 0.f;
+#pragma unroll 4
+    for (int c = 8 * lane; c < a.d; c += 256) {
+      const uint4 w0 = *reinterpret_cast<const uint4*>(r0 + c);
+      const uint4 w1 = *reinterpret_cast<const uint4*>(r1 + c);
+#pragma unroll
+      for (int i = 0; i < TG; ++i) {
+        const int t = i < nt ? t0 + i : t0;
+        const uint4 x = *reinterpret_cast<const uint4*>(a.X + t * a.ldx + c);
+        acc[0][i] += dot8(x, w0);
+        acc[1][i] += dot8(x, w1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TG; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        acc[0][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][i], o);
+        acc[1][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[1][i], o);
+      }
+      if (lane == 0 && i < nt) {
+        st_cluster_f32(mapa_shared(smem_u32(&logits[e0]), i), acc[0][i]);
+        if (two) st_cluster_f32(mapa_shared(smem_u32(&logits[e0 + 1]), i), acc[1][i]);
+      }
+    }
+  }
+  // x of these tokens: one half-warp per block of 128 columns
+  {
+    const int nb = (a.d + kFp8Block - 1) / kFp8Block;
+    const int h = rank * (R_THREADS / 16) + static_cast<int>(threadIdx.x >> 4);
+    for (int kb = h; kb - static_cast<int>((threadIdx.x >> 4) & 1) < nb; kb += R_CTAS * (R_THREADS / 16))
+      for (int t = t0; t < t0 + nt; t += 4)
+        fp8_quant_rows4(a.X, TG >= 4 ? a.T : t0 + nt, a.d, a.ldx, a.xq, a.xs, a.ld_x, t, kb);
+  }
+  cluster_sync_all();
+  if (warp != 0 || rank >= nt) return;
+
+  // Selection of token t0 + rank.  Keys order as the logits do; NaN comes last
+  // (key 1) and what has been taken is 0.
+  const int t = t0 + rank;
+  uint32_t key[kMoeMaxE / 32];
+  float lsum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMoeMaxE / 32; ++i) {
+    const int e = 32 * i + lane;
+    key[i] = 0u;
+    if (e < a.E) {
+      const float l = logits[e];
+      const uint32_t b = __float_as_uint(l);
+      key[i] = l != l ? 1u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    }
+  }
+  uint32_t mine_e = 0u;
+  float mine_l = 0.f, lmax = 0.f;
+  for (int j = 0; j < a.top_k; ++j) {
+    uint32_t best = 0u;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < kMoeMaxE / 32; ++i)
+      if (key[i] > best) {               // the first of equal keys: the lower index
+        best = key[i];
+        bi = i;
+      }
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+    const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * bi + lane : 0xFFFFu);
+#pragma unroll
+    for (int i = 0; i < kMoeMaxE / 32; ++i)
+      if (e == 32u * i + lane) key[i] = 0u;
+    const float l = logits[e];
+    if (j == 0) lmax = l;
+    if (lane == j) {
+      mine_e = e;
+      mine_l = l;
+    }
+  }
+  const float ex = lane < a.top_k ? expf(mine_l - lmax) : 0.f;
+  if (a.renorm) {
+    lsum = ex;
+  } else {
+    for (int e = lane; e < a.E; e += 32) lsum += expf(logits[e] - lmax);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, o);
+  if (lane < a.top_k) {
+    const int at = t * a.top_k + lane;
+    const float w = ex / lsum;
+    a.ids[at] = static_cast<int>(mine_e);
+    a.wts[at] = w;
+    if (a.ids_out) a.ids_out[at] = static_cast<int>(mine_e);
+    if (a.wts_out) a.wts_out[at] = w;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Experts
+// ---------------------------------------------------------------------------
+// How many ranges K is split into: the fewest steps of the longest CTA, a unit
+// counted as its K blocks and two more for its start and end.
+__host__ __device__ inline int moe_split(int units, int nkb, int most, int ctas) {
+  int best = 1, cost = 0x7FFFFFFF;
+  for (int s = 1; s <= most && s <= nkb; ++s) {
+    const int c = ((units * s + ctas - 1) / ctas) * ((nkb + s - 1) / s + 2);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+constexpr int M_THREADS = 256;     // weights, MMA, activations, idle, 4 epilogue warps
+constexpr int M_W_BYTES = 2 * 128 * 128;
+constexpr int M_UNITS = 4;         // units between the producer and the epilogue
+constexpr int M_CONSUMERS = 6;     // warps that read a unit: MMA, activations, epilogue
+
+struct MoeUnit {
+  int kind;          // 0: up, 1: down, 2: no more
+  int ex;            // index of the expert among those with tokens
+  int blk;           // up: unit of d_ff rows; down: 256 columns of y
+  int split;
+};
+
+template <int N>
+struct MoeSmem {
+  static constexpr int kStageBytes = M_W_BYTES + N * 128;
+  static constexpr int kStages = N == 16 ? 6 : 5;
+  static constexpr int kSaSlots = kStages + 2;      // as in the few-token product
+  uint8_t stage[kStages][kStageBytes];
+  alignas(16) float sa[kSaSlots][N];
+  uint64_t mask[kMoeMaxE];                          // tokens of each expert
+  uint16_t act_e[kMoeMaxE];                         // experts with tokens
+  uint16_t off[kMoeMaxE];                           // by expert: its first row among the pairs
+  uint16_t row_of[kMoeMaxT * kMoeMaxK];             // (token, choice) -> row
+  uint32_t amax[2][4][4];
+  MoeUnit unit[M_UNITS];
+  uint64_t unit_full[M_UNITS];
+  uint64_t unit_empty[M_UNITS];
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t sa_full[kSaSlots];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  int n_act, s_up, s_dn;
+  int last;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+
+// named barrier over `nthreads` threads that also tells all of them whether
+// any had a non-zero pred
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, uint32_t pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(pred), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+
+// global-memory writes of other SMs, seen through a counter, become visible to
+// this SM's TMA loads (and the reverse)
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Waits until *p >= target; bounded like the barrier waits.
+__device__ __forceinline__ bool counter_wait_bounded(const int* p, int target,
+                                                     volatile uint32_t* abort, uint32_t err_bit) {
+  if (ld_acquire(p) >= target) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (ld_acquire(p) >= target) return true;
+    if ((it & 15u) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > *static_cast<volatile uint64_t*>(&g_wait_limit_ns)) {
+        atomicOr(&g_device_error, err_bit);
+        *abort = 1u;
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float moe_silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+__device__ __forceinline__ float moe_gelu(float y) {
+  const float u = 0.7978845608028654f * (y + 0.044715f * y * y * y);
+  return y / (1.0f + expf(-2.0f * u));
+}
+
+// One block of 128 hidden rows of one expert, all its pairs, by the 128
+// epilogue threads: the ranges' sums joined in order, the activation, and the
+// e4m3 codes with their scale.
+template <bool kGated>
+__device__ __forceinline__ void moe_finish_h(const MoeArgs& a, uint32_t (&amax)[2][4][4], int off, int m,
+                                             int blk, int splits, int tid) {
+  const int row = blk * 128 + tid;
+  const bool in = row < a.ff;
+  const int64_t stride = static_cast<int64_t>(kGated ? 2 : 1) * a.ff;      // floats per pair
+  int buf = 0;
+  for (int p0 = 0; p0 < m; p0 += 4, buf ^= 1) {
+    float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) {
+      const float* ps = a.part_up + (static_cast<int64_t>(s) * a.pairs + off + p0) * stride + row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (in && p0 + i < m) {
+          if constexpr (kGated) {
+            g[i] += __ldcg(ps + i * stride);
+            u[i] += __ldcg(ps + i * stride + a.ff);
+          } else {
+            u[i] += __ldcg(ps + i * stride);
+          }
+        }
+      }
+    }
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = kGated ? moe_silu_mul(g[i], u[i]) : moe_gelu(u[i]);
+      const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+      if ((tid & 31) == 0) amax[buf][i][tid >> 5] = w;
+    }
+    named_bar_sync(1, 128);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p0 + i < m) {
+        const uint32_t eb = f8_scale_exp(max(max(amax[buf][i][0], amax[buf][i][1]),
+                                             max(amax[buf][i][2], amax[buf][i][3])));
+        const int64_t r = off + p0 + i;
+        if (in) {
+          const uint32_t c = eb == 0u ? 0u : cvt_e4m3x4(h[i] * f8_inv_scale(eb), 0.f, 0.f, 0.f);
+          a.hq[r * a.ff + row] = static_cast<uint8_t>(c);
+        }
+        if (tid == 0) a.hs[static_cast<int64_t>(blk) * a.pairs + r] = f8_scale(eb);
+      }
+    }
+  }
+}
+
+template <int N, bool kGated>
+__global__ void __launch_bounds__(M_THREADS, 1)
+    moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate,
+                       const __grid_constant__ CUtensorMap tm_up,
+                       const __grid_constant__ CUtensorMap tm_down,
+                       const __grid_constant__ CUtensorMap tm_xq,
+                       const __grid_constant__ CUtensorMap tm_hq, const __grid_constant__ MoeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  using Smem = MoeSmem<N>;
+  constexpr int NST = Smem::kStages;
+  Smem& sm = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  volatile uint32_t* abort_flag = &sm.abort_flag;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int nkb_d = (a.d + 127) / 128, nkb_f = (a.ff + 127) / 128;
+  const int up_units = kGated ? nkb_f : (nkb_f + 1) / 2;         // per expert
+  const int dn_tiles = (a.d + 255) / 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 2);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < Smem::kSaSlots; ++s) mbar_init(&sm.sa_full[s], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 4);
+    }
+    for (int u = 0; u < M_UNITS; ++u) {
+      mbar_init(&sm.unit_full[u], 1);
+      mbar_init(&sm.unit_empty[u], M_CONSUMERS);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0u;
+    fence_barrier_init();
+    if (kGated) prefetch_tmap(&tm_gate);
+    prefetch_tmap(&tm_up);
+    prefetch_tmap(&tm_down);
+    prefetch_tmap(&tm_xq);
+    prefetch_tmap(&tm_hq);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 4 * N);
+    tmem_relinquish();
+  }
+  for (int e = threadIdx.x; e < a.E; e += M_THREADS) sm.mask[e] = 0ull;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // The tokens of each expert as a bit mask (a token chooses an expert once at
+  // most), the experts that have any in ascending order, and the rows of their
+  // (token, expert) pairs: expert by expert, tokens ascending, each expert's
+  // first row a multiple of 4 so that its scales start on 16 bytes.
+  const int npairs = a.T * a.top_k;
+  for (int p = threadIdx.x; p < npairs; p += M_THREADS)
+    atomicOr(reinterpret_cast<unsigned long long*>(&sm.mask[a.ids[p]]), 1ull << (p / a.top_k));
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0, rows = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int m = e < a.E ? __popcll(sm.mask[e]) : 0;
+      const uint32_t any = __ballot_sync(0xFFFFFFFFu, m != 0);
+      int inc = (m + 3) & ~3;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (m != 0) {
+        const int at = n + __popc(any & ((1u << lane) - 1u));
+        sm.act_e[at] = static_cast<uint16_t>(e);
+        sm.off[e] = static_cast<uint16_t>(rows + inc - ((m + 3) & ~3));
+      }
+      n += __popc(any);
+      rows += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    if (lane == 0) {
+      sm.n_act = n;
+      sm.s_up = moe_split(n * up_units, nkb_d, a.most_up, static_cast<int>(gridDim.x));
+      sm.s_dn = moe_split(n * dn_tiles, nkb_f, a.most_dn, static_cast<int>(gridDim.x));
+    }
+  }
+  __syncthreads();
+  const int n_act = sm.n_act, s_up = sm.s_up, s_dn = sm.s_dn;
+  for (int p = threadIdx.x; p < npairs; p += M_THREADS) {
+    const int e = a.ids[p], t = p / a.top_k;
+    sm.row_of[p] = static_cast<uint16_t>(sm.off[e] + __popcll(sm.mask[e] & ((1ull << t) - 1ull)));
+  }
+  __syncthreads();
+  const int n_up = n_act * up_units * s_up;
+  const int n_all = n_up + dn_tiles * n_act * s_dn;
+  auto kb_lo = [](int nkb, int s, int splits) { return nkb * s / splits; };
+
+  if (warp == 0) {
+    // ================== weights (and the order of the units) ==============
+    int next = 0;
+    if (lane == 0) next = atomicAdd(a.ticket, 1);
+    next = __shfl_sync(0xFFFFFFFFu, next, 0);
+    uint32_t it = 0, u = 0;
+    bool ok = true;
+    while (ok) {
+      const int cur = next;
+      const int us = static_cast<int>(u % M_UNITS);
+      if (u >= M_UNITS && !warp_wait_bounded(&sm.unit_empty[us], ((u / M_UNITS) & 1u) ^ 1u, abort_flag,
+                                             DEVERR_TIMEOUT_PRODUCER))
+        break;
+      MoeUnit un;
+      if (cur < n_up) {
+        un.kind = 0;
+        un.split = cur % s_up;
+        un.blk = (cur / s_up) % up_units;
+        un.ex = cur / (s_up * up_units);
+      } else if (cur < n_all) {
+        const int v = cur - n_up;
+        un.kind = 1;
+        un.split = v % s_dn;
+        un.ex = (v / s_dn) % n_act;
+        un.blk = v / (s_dn * n_act);
+      } else {
+        un.kind = 2;
+        un.split = un.ex = un.blk = 0;
+      }
+      if (lane == 0) {
+        sm.unit[us] = un;
+        mbar_arrive(&sm.unit_full[us]);
+        if (un.kind != 2) next = atomicAdd(a.ticket, 1);     // used after this unit's tiles
+      }
+      __syncwarp();
+      if (un.kind == 2) break;
+      ++u;
+      const int e = sm.act_e[un.ex];
+      const int nkb = un.kind == 0 ? nkb_d : nkb_f;
+      const int splits = un.kind == 0 ? s_up : s_dn;
+      const int kb1 = kb_lo(nkb, un.split + 1, splits);
+      for (int kb = kb_lo(nkb, un.split, splits); kb < kb1; ++kb, ++it) {
+        const int s = static_cast<int>(it % NST);
+        if (it >= NST && !warp_wait_bounded(&sm.empty[s], ((it / NST) & 1u) ^ 1u, abort_flag,
+                                            DEVERR_TIMEOUT_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* st = sm.stage[s];
+          mbar_arrive_expect_tx(&sm.full[s], M_W_BYTES);
+          if (un.kind == 1) {
+            tma_load_3d(st, &tm_down, &sm.full[s], kb * 128, un.blk * 256, e);
+            tma_load_3d(st + 128 * 128, &tm_down, &sm.full[s], kb * 128, un.blk * 256 + 128, e);
+          } else if (kGated) {
+            tma_load_3d(st, &tm_gate, &sm.full[s], kb * 128, un.blk * 128, e);
+            tma_load_3d(st + 128 * 128, &tm_up, &sm.full[s], kb * 128, un.blk * 128, e);
+          } else {
+            tma_load_3d(st, &tm_up, &sm.full[s], kb * 128, un.blk * 256, e);
+            tma_load_3d(st + 128 * 128, &tm_up, &sm.full[s], kb * 128, un.blk * 256 + 128, e);
+          }
+        }
+        __syncwarp();
+      }
+      next = __shfl_sync(0xFFFFFFFFu, next, 0);
+    }
+    if (*abort_flag) spin_ns(200000);          // copies in flight land before teardown
+    __syncwarp();
+  } else if (warp == 2) {
+    // ======================== activations =================================
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t u = 0; ok; ++u) {
+      const int us = static_cast<int>(u % M_UNITS);
+      if (!warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag, DEVERR_TIMEOUT_PRODUCER))
+        break;
+      const MoeUnit un = sm.unit[us];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[us]);
+      if (un.kind == 2) break;
+      const int nkb = un.kind == 0 ? nkb_d : nkb_f;
+      const int splits = un.kind == 0 ? s_up : s_dn;
+      const int off = un.kind == 0 ? 0 : sm.off[sm.act_e[un.ex]];
+      const int cols = un.kind == 0 ? a.T : __popcll(sm.mask[sm.act_e[un.ex]]);
+      const uint32_t sa_bytes = static_cast<uint32_t>((cols + 3) & ~3) * 4u;
+      const float* sa = un.kind == 0 ? a.xs : a.hs + off;
+      const int64_t ld = un.kind == 0 ? a.ld_x : a.pairs;
+      if (un.kind == 1) {
+        const bool got = counter_wait_bounded(a.ready + un.ex, up_units, abort_flag,
+                                              DEVERR_TIMEOUT_PRODUCER);
+        if (!__all_sync(0xFFFFFFFFu, got)) break;
+        fence_proxy_async_global();
+      }
+      const int kb1 = kb_lo(nkb, un.split + 1, splits);
+      for (int kb = kb_lo(nkb, un.split, splits); kb < kb1; ++kb, ++it) {
+        const int s = static_cast<int>(it % NST);
+        const int q = static_cast<int>(it % Smem::kSaSlots);
+        if (it >= NST && !warp_wait_bounded(&sm.empty[s], ((it / NST) & 1u) ^ 1u, abort_flag,
+                                            DEVERR_TIMEOUT_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.full[s], N * 128);
+          tma_load_2d(sm.stage[s] + M_W_BYTES, un.kind == 0 ? &tm_xq : &tm_hq, &sm.full[s], kb * 128,
+                      off);
+          mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
+          bulk_load(sm.sa[q], sa + kb * ld, sa_bytes, &sm.sa_full[q]);
+        }
+        __syncwarp();
+      }
+    }
+    if (*abort_flag) spin_ns(200000);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ============================ MMA issuer ==============================
+    const uint64_t dw0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]));
+    const uint64_t dw1 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]) + 128 * 128);
+    const uint64_t dx0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]) + M_W_BYTES);
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t u = 0; ok; ++u) {
+      const int us = static_cast<int>(u % M_UNITS);
+      if (!warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag, DEVERR_TIMEOUT_MMA))
+        break;
+      const MoeUnit un = sm.unit[us];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[us]);
+      if (un.kind == 2) break;
+      const int nkb = un.kind == 0 ? nkb_d : nkb_f;
+      const int splits = un.kind == 0 ? s_up : s_dn;
+      const int nk = kb_lo(nkb, un.split + 1, splits) - kb_lo(nkb, un.split, splits);
+      for (int i = 0; i < nk; ++i, ++it) {
+        const int s = static_cast<int>(it % NST);
+        const uint32_t b = it & 1u;
+        if (!warp_wait_bounded(&sm.acc_empty[b], ((it >> 1) & 1u) ^ 1u, abort_flag, DEVERR_TIMEOUT_MMA) ||
+            !warp_wait_bounded(&sm.full[s], (it / NST) & 1u, abort_flag, DEVERR_TIMEOUT_MMA)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t so = static_cast<uint64_t>(s * (Smem::kStageBytes >> 4));
+          const uint32_t d0 = tmem + b * 2 * N;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            mma_f8(d0, dw0 + so + 2 * kk, dx0 + so + 2 * kk, idesc_f8(128, N), kk != 0);
+            mma_f8(d0 + N, dw1 + so + 2 * kk, dx0 + so + 2 * kk, idesc_f8(128, N), kk != 0);
+          }
+          tc_commit(&sm.empty[s]);
+          tc_commit(&sm.acc_full[b]);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) tc_commit(&sm.drain);
+    __syncwarp();
+    mbar_wait_bounded(&sm.drain, 0u, nullptr, DEVERR_TIMEOUT_MMA);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ============================ epilogue ================================
+    // The four warps agree at every barrier on whether one of them gave up
+    // (named_bar_or), so none is left waiting for another.
+    const int sp = warp & 3;
+    const int tid = 32 * sp + lane;                    // the tile row of this thread
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
+    uint32_t it = 0;
+    for (uint32_t u = 0;; ++u) {
+      const int us = static_cast<int>(u % M_UNITS);
+      bool ok = warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag,
+                                  DEVERR_TIMEOUT_EPILOGUE);
+      if (named_bar_or(1, 128, !ok)) break;
+      const MoeUnit un = sm.unit[us];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[us]);
+      if (un.kind == 2) break;
+      const int e = sm.act_e[un.ex];
+      const int off = sm.off[e];
+      const uint64_t mk = sm.mask[e];
+      const int m = __popcll(mk);
+      const int nkb = un.kind == 0 ? nkb_d : nkb_f;
+      const int splits = un.kind == 0 ? s_up : s_dn;
+      const int k0 = kb_lo(nkb, un.split, splits), k1 = kb_lo(nkb, un.split + 1, splits);
+      // the two tiles' scales
+      const float *sb0, *sb1;
+      int second = 1;                                  // the second tile has rows
+      if (un.kind == 1) {
+        second = un.blk * 256 + 128 < a.d;
+        sb0 = a.down_s + (static_cast<int64_t>(e) * nkb_d + 2 * un.blk) * nkb_f;
+        sb1 = second ? sb0 + nkb_f : sb0;
+      } else if (kGated) {
+        sb0 = a.gate_s + (static_cast<int64_t>(e) * nkb_f + un.blk) * nkb_d;
+        sb1 = a.up_s + (static_cast<int64_t>(e) * nkb_f + un.blk) * nkb_d;
+      } else {
+        second = un.blk * 256 + 128 < a.ff;
+        sb0 = a.up_s + (static_cast<int64_t>(e) * nkb_f + 2 * un.blk) * nkb_d;
+        sb1 = second ? sb0 + nkb_d : sb0;
+      }
+      float2 acc[2][N / 2];
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) acc[0][j] = acc[1][j] = make_float2(0.f, 0.f);
+      float s0 = sb0[k0], s1 = sb1[k0];
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int q = static_cast<int>(it % Smem::kSaSlots);
+        const uint32_t b = it & 1u;
+        const float c0 = s0, c1 = s1;
+        if (kb + 1 < k1) {
+          s0 = sb0[kb + 1];
+          s1 = sb1[kb + 1];
+        }
+        if (!warp_wait_bounded(&sm.sa_full[q], (it / Smem::kSaSlots) & 1u, abort_flag,
+                               DEVERR_TIMEOUT_EPILOGUE) ||
+            !warp_wait_bounded(&sm.acc_full[b], (it >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float sb = h ? c1 : c0;
+#pragma unroll
+          for (int c = 0; c < N / 16; ++c) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(taddr + b * 2 * N + h * N + 16 * c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][16 * c + 4 * j]);
+              float2& a0 = acc[h][8 * c + 2 * j];
+              float2& a1 = acc[h][8 * c + 2 * j + 1];
+              a0 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
+                              make_float2(s4.x * sb, s4.y * sb), a0);
+              a1 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
+                              make_float2(s4.z * sb, s4.w * sb), a1);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+      }
+      if (named_bar_or(1, 128, !ok)) break;
+      // this unit's sums, pair by pair
+      if (un.kind == 0) {
+        const int r0 = (kGated ? un.blk : 2 * un.blk) * 128 + tid;
+        const int64_t stride = static_cast<int64_t>(kGated ? 2 : 1) * a.ff;
+        float* p = a.part_up + (static_cast<int64_t>(un.split) * a.pairs + off) * stride + r0;
+        const bool in0 = r0 < a.ff, in1 = kGated ? in0 : r0 + 128 < a.ff;
+        const int64_t second_at = kGated ? a.ff : 128;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if ((mk >> c) & 1ull) {
+            if (in0) __stcg(p, (c & 1) ? acc[0][c >> 1].y : acc[0][c >> 1].x);
+            if (in1) __stcg(p + second_at, (c & 1) ? acc[1][c >> 1].y : acc[1][c >> 1].x);
+            p += stride;
+          }
+        }
+      } else {
+        const int r0 = un.blk * 256 + tid;
+        float* p = a.part_dn + (static_cast<int64_t>(un.split) * a.pairs + off) * a.d + r0;
+        const bool in0 = r0 < a.d, in1 = r0 + 128 < a.d;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (c < m) {
+            if (in0) __stcg(p, (c & 1) ? acc[0][c >> 1].y : acc[0][c >> 1].x);
+            if (in1) __stcg(p + 128, (c & 1) ? acc[1][c >> 1].y : acc[1][c >> 1].x);
+            p += a.d;
+          }
+        }
+      }
+      // the last of the units that make up a block finishes it
+      __threadfence();
+      named_bar_sync(1, 128);
+      if (tid == 0) {
+        int* ctr = un.kind == 0 ? a.up_done + un.ex * up_units + un.blk : a.dn_done + un.blk;
+        const int all = un.kind == 0 ? s_up : n_act * s_dn;
+        sm.last = atomicAdd(ctr, 1) == all - 1;
+        __threadfence();
+      }
+      named_bar_sync(1, 128);
+      if (!sm.last) continue;
+      if (un.kind == 0) {
+        if constexpr (kGated) {
+          moe_finish_h<true>(a, sm.amax, off, m, un.blk, s_up, tid);
+        } else {
+          moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk, s_up, tid);
+          named_bar_sync(1, 128);
+          if (second) moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk + 1, s_up, tid);
+        }
+        fence_proxy_async_global();
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (tid == 0) {
+          __threadfence();
+          atomicAdd(a.ready + un.ex, 1);
+        }
+      } else {
+        const int col = un.blk * 256 + 2 * tid;
+        if (col < a.d) {
+          for (int t = 0; t < a.T; ++t) {
+            float2 y = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int j = 0; j < a.top_k; ++j) {
+              const int pr = t * a.top_k + j;
+              const float* p = a.part_dn + static_cast<int64_t>(sm.row_of[pr]) * a.d + col;
+              float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+              for (int s = 1; s < s_dn; ++s) {
+                const float2 w = __ldcg(reinterpret_cast<const float2*>(p + s * a.pairs * a.d));
+                v.x += w.x;
+                v.y += w.y;
+              }
+              const float wt = a.wts[pr];
+              y.x = fmaf(wt, v.x, y.x);
+              y.y = fmaf(wt, v.y, y.y);
+            }
+            const int64_t at = t * a.ldy + col;
+            if (a.y_f32)
+              *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + at) = y;
+            else
+              *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.Y) + at) =
+                  __floats2bfloat162_rn(y.x, y.y);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 4 * N);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// A stack of matrices of e4m3 codes in boxes of 128 x 128.
+static bool make_tmap_stack(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t n) {
+  PFN_encodeTiled enc = get_encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {cols, rows, n};
+  cuuint64_t strides[2] = {cols, cols * rows};
+  cuuint32_t box[3] = {128, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace, from the sizes alone (no device query: the same on every device).
+MoeLayout moe_layout(int64_t T, int64_t d, int64_t ff, int64_t E, int64_t top_k, bool gated) {
+  MoeLayout l;
+  constexpr int kCtas = 148;
+  const int64_t P = T * top_k;
+  l.pairs = round_up(P + 3 * (E < P ? E : P), 4);
+  l.ld_x = round_up(T, 4);
+  const int64_t nkb_d = (d + 127) / 128, nkb_f = (ff + 127) / 128;
+  const int64_t up_units = gated ? nkb_f : (nkb_f + 1) / 2, dn_tiles = (d + 255) / 256;
+  // at least top_k experts have tokens; more splits than two per CTA gain nothing
+  auto most = [&](int64_t units, int64_t nkb) {
+    int64_t s = (2 * kCtas + top_k * units - 1) / (top_k * units);
+    s = s < kMoeMaxSplit ? s : kMoeMaxSplit;
+    return s < nkb ? s : nkb;
+  };
+  l.most_up = static_cast<int>(most(up_units, nkb_d));
+  l.most_dn = static_cast<int>(most(dn_tiles, nkb_f));
+  const int64_t nE = E < P ? E : P;
+  l.up_done = 0;
+  l.ready = l.up_done + nE * up_units;
+  l.dn_done = l.ready + nE;
+  l.ticket = l.dn_done + dn_tiles;
+  l.ncounters = l.ticket + 1;
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t p = at;
+    at += static_cast<size_t>(round_up(bytes, 1024));
+    return p;
+  };
+  l.xq = take(T * d);
+  l.xs = take(nkb_d * l.ld_x * 4);
+  l.ids = take(P * 4);
+  l.wts = take(P * 4);
+  l.hq = take(l.pairs * ff);
+  l.hs = take(nkb_f * l.pairs * 4);
+  l.part_up = take(l.most_up * l.pairs * (gated ? 2 : 1) * ff * 4);
+  l.part_dn = take(l.most_dn * l.pairs * d * 4);
+  l.counters = take(l.ncounters * 4);
+  l.total = at;
+  return l;
+}
+
+template <int N, bool kGated>
+static cudaError_t moe_attr() {
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(moe_experts_kernel<N, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(MoeSmem<N>) + 1024));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
+  return e;
+}
+
+template <int N, bool kGated>
+static cudaError_t run_moe_experts(const MoePlan& p, cudaStream_t stream) {
+  return launch_pdl(moe_experts_kernel<N, kGated>, dim3(p.ctas), dim3(M_THREADS),
+                    sizeof(MoeSmem<N>) + 1024, stream, p.tm_gate, p.tm_up, p.tm_down, p.tm_xq, p.tm_hq,
+                    p.a);
+}
+
+cudaError_t plan_moe(const MoeArgs& a, int64_t E, const uint8_t* gate, const uint8_t* up,
+                     const uint8_t* down, bool gated, MoePlan* p) {
+  memset(p, 0, sizeof(*p));
+  p->a = a;
+  p->gated = gated;
+  p->n = a.T <= 16 ? 16 : a.T <= 32 ? 32 : 64;
+  p->ctas = device_num_sms();
+  if (p->ctas <= 0) return cudaErrorInvalidDevice;
+  cudaError_t e = gated ? (p->n == 16 ? moe_attr<16, true>() : p->n == 32 ? moe_attr<32, true>() : moe_attr<64, true>())
+                        : (p->n == 16 ? moe_attr<16, false>() : p->n == 32 ? moe_attr<32, false>() : moe_attr<64, false>());
+  if (e != cudaSuccess) return e;
+  if ((gated && !make_tmap_stack(&p->tm_gate, gate, a.d, a.ff, E)) ||
+      !make_tmap_stack(&p->tm_up, up, a.d, a.ff, E) || !make_tmap_stack(&p->tm_down, down, a.ff, a.d, E) ||
+      !make_tmap(&p->tm_xq, a.xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.d, a.T, a.d, p->n) ||
+      !make_tmap(&p->tm_hq, a.hq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.ff, a.pairs, a.ff, p->n))
+    return cudaErrorInvalidValue;
+  if (!gated) p->tm_gate = p->tm_up;
+  return cudaSuccess;
+}
+
+cudaError_t run_moe(const MoePlan& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  const int tg = p.a.T == 1 ? 1 : 4;
+  cfg.gridDim = dim3(static_cast<unsigned>(R_CTAS * ((p.a.T + tg - 1) / tg)));
+  cfg.blockDim = dim3(R_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = R_CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + static_cast<unsigned>(pdl_attrs(&attr[1]));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tg == 1 ? moe_route_kernel<1> : moe_route_kernel<4>, p.a);
+  if (e != cudaSuccess) return e;
+  if (p.gated)
+    return p.n == 16 ? run_moe_experts<16, true>(p, stream)
+                     : p.n == 32 ? run_moe_experts<32, true>(p, stream) : run_moe_experts<64, true>(p, stream);
+  return p.n == 16 ? run_moe_experts<16, false>(p, stream)
+                   : p.n == 32 ? run_moe_experts<32, false>(p, stream) : run_moe_experts<64, false>(p, stream);
+}
+
+}  // namespace w4a4

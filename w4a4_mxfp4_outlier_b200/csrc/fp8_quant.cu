@@ -19,19 +19,16 @@ namespace w4a4 {
 
 // One half-warp per (4 rows, one block): 16 lanes x 16 bytes cover a row's
 // 128 columns, the four rows' loads are independent, and the four scales of
-// consecutive tokens leave as one 16-byte store (scale is [blocks][ld_scale]).
-__global__ void __launch_bounds__(256) fp8_quant_act_kernel(const __nv_bfloat16* __restrict__ X,
-                                                            int64_t T, int d, int64_t ldx,
-                                                            uint8_t* __restrict__ q,
-                                                            float* __restrict__ scale,
-                                                            int64_t ld_scale) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
-  const int kb = blockIdx.y * (blockDim.x >> 4) + hw;
+// consecutive tokens leave as one 16-byte store (scale is [blocks][ld_scale],
+// ld_scale a multiple of 4 and at least T rounded up to 4).  Called by whole
+// warps; a half-warp with kb outside [0, nb) only takes part in the shuffles.
+__device__ __forceinline__ void fp8_quant_rows4(const __nv_bfloat16* __restrict__ X, int64_t T, int d,
+                                                int64_t ldx, uint8_t* __restrict__ q,
+                                                float* __restrict__ scale, int64_t ld_scale,
+                                                int64_t t0, int kb) {
+  const int hl = threadIdx.x & 15;
   const int nb = (d + kFp8Block - 1) / kFp8Block;
   const int col = kb * kFp8Block + 8 * hl;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 4;
   const bool in = kb < nb && col < d;
   uint4 v[4];
 #pragma unroll
@@ -62,11 +59,20 @@ __global__ void __launch_bounds__(256) fp8_quant_act_kernel(const __nv_bfloat16*
       *reinterpret_cast<uint2*>(q + (t0 + r) * d + col) = make_uint2(c0, c1);
     }
   }
-  if (hl == 0 && kb < nb) {
-    // ld_scale is a multiple of 4 and at least T rounded up to 4
+  if (hl == 0 && kb < nb)
     *reinterpret_cast<float4*>(scale + kb * ld_scale + t0) =
         make_float4(sc[0], t0 + 1 < T ? sc[1] : 0.f, t0 + 2 < T ? sc[2] : 0.f, t0 + 3 < T ? sc[3] : 0.f);
-  }
+}
+
+__global__ void __launch_bounds__(256) fp8_quant_act_kernel(const __nv_bfloat16* __restrict__ X,
+                                                            int64_t T, int d, int64_t ldx,
+                                                            uint8_t* __restrict__ q,
+                                                            float* __restrict__ scale,
+                                                            int64_t ld_scale) {
+  pdl_wait();
+  pdl_launch_dependents();
+  fp8_quant_rows4(X, T, d, ldx, q, scale, ld_scale, static_cast<int64_t>(blockIdx.x) * 4,
+                  static_cast<int>(blockIdx.y * (blockDim.x >> 4) + (threadIdx.x >> 4)));
 }
 
 cudaError_t launch_fp8_quant_act(const void* X, int64_t T, int64_t d, int64_t ldx, uint8_t* q,

@@ -13,4 +13,5 @@
 #include "ffn.cu"
 #include "fp8_quant.cu"
 #include "fp8_gemm.cu"
+#include "fp8_moe.cu"
 #include "fp8_api.cu"
