@@ -41,6 +41,7 @@ struct FewSmem {
   static constexpr int kSaSlots = kStages + 2;
   uint8_t stage[kStages][kStageBytes];
   alignas(16) float sa[kSaSlots][N];
+  float sb[kSaSlots];
   uint64_t full[kStages];
   uint64_t empty[kStages];
   uint64_t sa_full[kSaSlots];
@@ -118,9 +119,11 @@ __global__ void __launch_bounds__(F_THREADS, 2)
     pdl_wait();
     pdl_launch_dependents();
     uint32_t issued = 0;
+    WarpRun sb(args.sb + static_cast<int64_t>(blockIdx.x) * args.nkb + kb0, nk);
     for (int i = 0; i < nk; ++i) {
       const int s = i % NST;
       const int q = i % Smem::kSaSlots;
+      const float sbi = sb.get(i);
       if (i >= NST && !warp_wait_bounded(&sm.empty[s], ((i / NST) & 1) ^ 1u, abort_flag,
                                          DEVERR_TIMEOUT_PRODUCER))
         break;
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(F_THREADS, 2)
           tma_load_2d(sm.stage[s], &tm_w, &sm.full[s], (kb0 + i) * 128, n0);
         }
         tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, t0);
+        sm.sb[q] = sbi;
         mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
         bulk_load(sm.sa[q], args.sa + (kb0 + i) * args.ld_sa + t0, sa_bytes, &sm.sa_full[q]);
       }
@@ -177,19 +181,17 @@ __global__ void __launch_bounds__(F_THREADS, 2)
     pdl_wait();
     const int sp = warp & 3;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
-    const float* sbp = args.sb + static_cast<int64_t>(blockIdx.x) * args.nkb + kb0;
     float2 acc[N / 2];
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-    float sb = nk > 0 ? *sbp : 0.f;
     for (int i = 0; i < nk; ++i) {
       const int q = i % Smem::kSaSlots;
       const uint32_t b = i & 1;
-      const float sb_next = i + 1 < nk ? sbp[i + 1] : 0.f;
       if (!warp_wait_bounded(&sm.sa_full[q], (i / Smem::kSaSlots) & 1u, abort_flag,
                              DEVERR_TIMEOUT_EPILOGUE) ||
           !warp_wait_bounded(&sm.acc_full[b], (i >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
         break;
+      const float sb = sm.sb[q];
       tc_fence_after();
       constexpr int CH = N < 32 ? 16 : 32;
 #pragma unroll
@@ -212,7 +214,6 @@ __global__ void __launch_bounds__(F_THREADS, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
-      sb = sb_next;
     }
     // this CTA's sums, [token][channel], over the ring: the last accumulator is
     // complete, so every tile has arrived and been read
@@ -268,10 +269,15 @@ constexpr int Q_STAGE_BYTES = 2 * Q_HALF;
 constexpr int Q_THREADS = 384;                        // producer, MMA, 2 idle, 8 epilogue warps
 constexpr int Q_EPI_WARPS = 8;
 constexpr int Q_GROUP_M = 16;
+constexpr int Q_SA_GROUP = 8;
 
 struct Fp8PairSmem {
   uint8_t stage[Q_STAGES][Q_STAGE_BYTES];
   alignas(1024) uint8_t epi[Q_EPI_WARPS][2][1024];
+  // scales of the CTA's own 128 tokens, for groups of 8 K blocks in turn
+  alignas(16) float sa[2][Q_SA_GROUP][128];
+  uint64_t sa_full[2];
+  uint64_t sa_empty[2];
   uint64_t full[Q_STAGES];      // leader's counts the bytes of both CTAs
   uint64_t empty[Q_STAGES];     // both CTAs: MMA commit, multicast
   uint64_t acc_full[2];         // both CTAs: MMA commit, multicast
@@ -313,6 +319,10 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.sa_full[s], 1);
+      mbar_init(&sm.sa_empty[s], Q_EPI_WARPS);
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.acc_full[b], 1);
       mbar_init(&sm.acc_empty[b], 2 * Q_EPI_WARPS);
@@ -341,14 +351,34 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
     setmaxnreg_dec<56>();
     if (warp == 0) {
       // ============================ TMA producer (both CTAs) ==============
-      uint32_t issued = 0, it = 0, s = 0, ph = 0;
+      uint32_t issued = 0, it = 0, s = 0, ph = 0, grp = 0;
       bool ok = true;
       for (int t = pair; t < ntiles && ok; t += npairs) {
         int tm, tn;
         tile_coords<Q_GROUP_M>(t, args.tiles_m, args.tiles_n, tm, tn);
         const int m_rows = tm * 256 + 128 * static_cast<int>(rank);
         const int n_rows = tn * 256 + 128 * static_cast<int>(rank);
+        const int rows = args.T - m_rows < 128 ? args.T - m_rows : 128;
+        const uint32_t sa_bytes = rows > 0 ? static_cast<uint32_t>((rows + 3) & ~3) * 4u : 0u;
         for (int kb = 0; kb < nkb; ++kb, ++it) {
+          if (kb % Q_SA_GROUP == 0) {
+            const uint32_t q = grp & 1u;
+            if (grp >= 2 && !warp_wait_bounded(&sm.sa_empty[q], ((grp >> 1) & 1u) ^ 1u, abort_flag,
+                                               DEVERR_TIMEOUT_PRODUCER)) {
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              const int n = nkb - kb < Q_SA_GROUP ? nkb - kb : Q_SA_GROUP;
+              mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes * n);
+              if (sa_bytes)
+                for (int i = 0; i < n; ++i)
+                  bulk_load(sm.sa[q][i], args.sa + (kb + i) * args.ld_sa + m_rows, sa_bytes,
+                            &sm.sa_full[q]);
+            }
+            __syncwarp();
+            ++grp;
+          }
           if (it >= Q_STAGES &&
               !warp_wait_bounded(&sm.empty[s], ph ^ 1u, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
             ok = false;
@@ -375,10 +405,10 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
             mbar_wait_bounded(&sm.full[i % Q_STAGES], (i / Q_STAGES) & 1u, nullptr,
                               DEVERR_TIMEOUT_PRODUCER);
         }
-        spin_ns(50000);            // the peer CTA's copies land on the leader's barriers
+        spin_ns(50000);   // scales, and the peer CTA's copies, which land on the leader's barriers
       }
       __syncwarp();
-    } else if (warp == 1 && rank == 0) {
+    } else if (rank == 0 && warp == 1) {
       // ============================ MMA issuer (leader) ===================
       constexpr uint64_t STAGE_DESC = Q_STAGE_BYTES >> 4;
       constexpr uint32_t ID = idesc_f8(256, 256);
@@ -390,9 +420,9 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
       for (int t = pair; t < ntiles && ok; t += npairs) {
         for (int kb = 0; kb < nkb; ++kb, ++g) {
           const uint32_t b = g & 1u;
-          if (!warp_wait_bounded(&sm.acc_empty[b], ((g >> 1) & 1u) ^ 1u, abort_flag,
-                                 DEVERR_TIMEOUT_MMA) ||
-              !warp_wait_bounded(&sm.full[s], ph, abort_flag, DEVERR_TIMEOUT_MMA)) {
+          if (!warp_wait_bounded(&sm.full[s], ph, abort_flag, DEVERR_TIMEOUT_MMA) ||
+              !warp_wait_bounded(&sm.acc_empty[b], ((g >> 1) & 1u) ^ 1u, abort_flag,
+                                 DEVERR_TIMEOUT_MMA)) {
             ok = false;
             break;
           }
@@ -403,8 +433,8 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
             mma_f8_pair(d, da0 + soff + 2, db0 + soff + 2, ID, 1u);
             mma_f8_pair(d, da0 + soff + 4, db0 + soff + 4, ID, 1u);
             mma_f8_pair(d, da0 + soff + 6, db0 + soff + 6, ID, 1u);
-            tc_commit_pair_multicast(&sm.empty[s], 0x3);
             tc_commit_pair_multicast(&sm.acc_full[b], 0x3);
+            tc_commit_pair_multicast(&sm.empty[s], 0x3);
           }
           __syncwarp();
           if (++s == Q_STAGES) {
@@ -431,54 +461,74 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(&sm.acc_empty[0]), 0);
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16) + 128 * half;
     const uint32_t stg = smem_u32(sm.epi[ew]);
-    uint32_t g = 0, buf = 0;
-    bool ok = true;
-    for (int t = pair; t < ntiles && ok; t += npairs) {
+    uint32_t g = 0, buf = 0, grp = 0;
+    for (int t = pair; t < ntiles; t += npairs) {
       int tm, tn;
       tile_coords<Q_GROUP_M>(t, args.tiles_m, args.tiles_n, tm, tn);
       const int row0 = tm * 256 + 128 * static_cast<int>(rank) + 32 * sp;
-      const int row = row0 + lane;
       const int nblk = tn * 2 + half;
-      const bool rin = row < args.T, nin = nblk * 128 < args.d_out;
-      const float* sap = args.sa + row;
-      const float* sbp = args.sb + static_cast<int64_t>(nblk) * nkb;
+      // (a block past d_out reads nothing; rows past T have any scale, and are not stored)
+      WarpRun sbr(args.sb + static_cast<int64_t>(nblk) * nkb, nblk * 128 < args.d_out ? nkb : 0);
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      float sa = rin ? *sap : 0.f;
-      float sb = nin ? *sbp : 0.f;
+      // What bounds the kernel: the tensor cores need 560 cycles per K block
+      // (measured without this loop: 190 us at T = 4096, 5120 -> 13824), this
+      // loop about 850 (260 us), of which the additions themselves take 330
+      // (100 FMAs per cycle and SM).  Measured and no faster: 16 warps of 64
+      // columns (268 us), MMAs of 128 columns with a buffer pair per half (267),
+      // one 32-column load at a time (276), scalar FMAs (283), the next block's
+      // loads before the last additions (299).  A wait that fails (it ends in
+      // bounded time, and all later ones then fail at once) only clears `ok`,
+      // which is looked at once per tile.
+      bool ok = true;
+      float m = 0.f;
+      uint32_t r[2][32];
+      auto add = [&](int c, float w) {
+        const float2 m2 = make_float2(w, w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          acc[16 * c + j] = __ffma2_rn(make_float2(__uint_as_float(r[c & 1][2 * j]),
+                                                   __uint_as_float(r[c & 1][2 * j + 1])),
+                                       m2, acc[16 * c + j]);
+      };
+      // scale of K block kb, and its sums complete
+      auto next_block = [&](int kb, uint32_t gk) {
+        const uint32_t q = grp & 1u;
+        const int qi = kb % Q_SA_GROUP;
+        if (qi == 0)
+          ok &= mbar_wait_bounded(&sm.sa_full[q], (grp >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+        m = sm.sa[q][qi][32 * sp + lane] * sbr.get(kb);
+        ok &= mbar_wait_bounded(&sm.acc_full[gk & 1u], (gk >> 1) & 1u, abort_flag,
+                                DEVERR_TIMEOUT_EPILOGUE);
+        __syncwarp();
+        tc_fence_after();
+        if (qi == Q_SA_GROUP - 1 || kb + 1 == nkb) {     // (all lanes have read their scale)
+          if (lane == 0) mbar_arrive(&sm.sa_empty[q]);
+          ++grp;
+        }
+      };
       for (int kb = 0; kb < nkb; ++kb, ++g) {
         const uint32_t b = g & 1u;
-        const float m = sa * sb;
-        const bool more = kb + 1 < nkb;
-        sa = rin && more ? sap[(kb + 1) * args.ld_sa] : 0.f;
-        sb = nin && more ? sbp[kb + 1] : 0.f;
-        if (!warp_wait_bounded(&sm.acc_full[b], (g >> 1) & 1u, abort_flag,
-                               DEVERR_TIMEOUT_EPILOGUE)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float2 m2 = make_float2(m, m);
         const uint32_t ta = taddr + 256u * b;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(ta + 32 * c, r);
-          tmem_ld_wait();
-          if (c == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8u * b);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[16 * c + j] = __ffma2_rn(
-                make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), m2,
-                acc[16 * c + j]);
-        }
+        next_block(kb, g);
+        tmem_ld_32x32b_x32(ta, r[0]);
+        tmem_ld_32x32b_x32(ta + 32, r[1]);
+        tmem_ld_wait_for(r[0]);
+        tmem_ld_waited(r[1]);
+        add(0, m);
+        tmem_ld_32x32b_x32(ta + 64, r[0]);
+        add(1, m);
+        tmem_ld_32x32b_x32(ta + 96, r[1]);
+        tmem_ld_wait_for(r[0]);
+        tmem_ld_waited(r[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(acc_empty_leader + 8u * b);
+        add(2, m);
+        add(3, m);
       }
-      if (!ok) break;
+      if (__any_sync(0xFFFFFFFFu, !ok)) break;
       // Y through staging blocks of 16 rows x 64 bytes (64-byte swizzle), as
       // the dual-branch GEMM stores it: 32 bf16 or 16 f32 columns a block,
       // two blocks in turn

@@ -210,6 +210,7 @@ struct MoeSmem {
   static constexpr int kSaSlots = kStages + 2;      // as in the few-token product
   uint8_t stage[kStages][kStageBytes];
   alignas(16) float sa[kSaSlots][N];
+  float2 sb[kSaSlots];                              // scales of the two weight tiles
   uint64_t mask[kMoeMaxE];                          // tokens of each expert
   uint16_t act_e[kMoeMaxE];                         // experts with tokens
   uint16_t off[kMoeMaxE];                           // by expert: its first row among the pairs
@@ -516,16 +517,31 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       const uint32_t sa_bytes = static_cast<uint32_t>((cols + 3) & ~3) * 4u;
       const float* sa = un.kind == 0 ? a.xs : a.hs + off;
       const int64_t ld = un.kind == 0 ? a.ld_x : a.pairs;
+      // the two tiles' scales; a second tile without rows takes the first one's
+      const int e = sm.act_e[un.ex];
+      const float *sb0, *sb1;
+      if (un.kind == 1) {
+        sb0 = a.down_s + (static_cast<int64_t>(e) * nkb_d + 2 * un.blk) * nkb_f;
+        sb1 = 2 * un.blk + 1 < nkb_d ? sb0 + nkb_f : sb0;
+      } else if (kGated) {
+        sb0 = a.gate_s + (static_cast<int64_t>(e) * nkb_f + un.blk) * nkb_d;
+        sb1 = a.up_s + (static_cast<int64_t>(e) * nkb_f + un.blk) * nkb_d;
+      } else {
+        sb0 = a.up_s + (static_cast<int64_t>(e) * nkb_f + 2 * un.blk) * nkb_d;
+        sb1 = 2 * un.blk + 1 < nkb_f ? sb0 + nkb_d : sb0;
+      }
+      const int k0 = kb_lo(nkb, un.split, splits), k1 = kb_lo(nkb, un.split + 1, splits);
+      WarpRun r0(sb0 + k0, k1 - k0), r1(sb1 + k0, k1 - k0);
       if (un.kind == 1) {
         const bool got = counter_wait_bounded(a.ready + un.ex, up_units, abort_flag,
                                               DEVERR_TIMEOUT_PRODUCER);
         if (!__all_sync(0xFFFFFFFFu, got)) break;
         fence_proxy_async_global();
       }
-      const int kb1 = kb_lo(nkb, un.split + 1, splits);
-      for (int kb = kb_lo(nkb, un.split, splits); kb < kb1; ++kb, ++it) {
+      for (int kb = k0; kb < k1; ++kb, ++it) {
         const int s = static_cast<int>(it % NST);
         const int q = static_cast<int>(it % Smem::kSaSlots);
+        const float2 sb2 = make_float2(r0.get(kb - k0), r1.get(kb - k0));
         if (it >= NST && !warp_wait_bounded(&sm.empty[s], ((it / NST) & 1u) ^ 1u, abort_flag,
                                             DEVERR_TIMEOUT_PRODUCER)) {
           ok = false;
@@ -535,6 +551,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
           mbar_arrive_expect_tx(&sm.full[s], N * 128);
           tma_load_2d(sm.stage[s] + M_W_BYTES, un.kind == 0 ? &tm_xq : &tm_hq, &sm.full[s], kb * 128,
                       off);
+          sm.sb[q] = sb2;
           mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
           bulk_load(sm.sa[q], sa + kb * ld, sa_bytes, &sm.sa_full[q]);
         }
@@ -612,33 +629,12 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       const int nkb = un.kind == 0 ? nkb_d : nkb_f;
       const int splits = un.kind == 0 ? s_up : s_dn;
       const int k0 = kb_lo(nkb, un.split, splits), k1 = kb_lo(nkb, un.split + 1, splits);
-      // the two tiles' scales
-      const float *sb0, *sb1;
-      int second = 1;                                  // the second tile has rows
-      if (un.kind == 1) {
-        second = un.blk * 256 + 128 < a.d;
-        sb0 = a.down_s + (static_cast<int64_t>(e) * nkb_d + 2 * un.blk) * nkb_f;
-        sb1 = second ? sb0 + nkb_f : sb0;
-      } else if (kGated) {
-        sb0 = a.gate_s + (static_cast<int64_t>(e) * nkb_f + un.blk) * nkb_d;
-        sb1 = a.up_s + (static_cast<int64_t>(e) * nkb_f + un.blk) * nkb_d;
-      } else {
-        second = un.blk * 256 + 128 < a.ff;
-        sb0 = a.up_s + (static_cast<int64_t>(e) * nkb_f + 2 * un.blk) * nkb_d;
-        sb1 = second ? sb0 + nkb_d : sb0;
-      }
       float2 acc[2][N / 2];
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) acc[0][j] = acc[1][j] = make_float2(0.f, 0.f);
-      float s0 = sb0[k0], s1 = sb1[k0];
       for (int kb = k0; kb < k1; ++kb, ++it) {
         const int q = static_cast<int>(it % Smem::kSaSlots);
         const uint32_t b = it & 1u;
-        const float c0 = s0, c1 = s1;
-        if (kb + 1 < k1) {
-          s0 = sb0[kb + 1];
-          s1 = sb1[kb + 1];
-        }
         if (!warp_wait_bounded(&sm.sa_full[q], (it / Smem::kSaSlots) & 1u, abort_flag,
                                DEVERR_TIMEOUT_EPILOGUE) ||
             !warp_wait_bounded(&sm.acc_full[b], (it >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) {
@@ -646,9 +642,10 @@ __global__ void __launch_bounds__(M_THREADS, 1)
           break;
         }
         tc_fence_after();
+        const float2 sb2 = sm.sb[q];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float sb = h ? c1 : c0;
+          const float sb = h ? sb2.y : sb2.x;
 #pragma unroll
           for (int c = 0; c < N / 16; ++c) {
             uint32_t r[16];
@@ -716,7 +713,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         } else {
           moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk, s_up, tid);
           named_bar_sync(1, 128);
-          if (second) moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk + 1, s_up, tid);
+          if (2 * un.blk + 1 < nkb_f) moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk + 1, s_up, tid);
         }
         fence_proxy_async_global();
         __threadfence();
