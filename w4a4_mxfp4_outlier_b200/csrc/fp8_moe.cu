@@ -39,7 +39,8 @@ constexpr int kMoeMaxSplit = 8;
 // Router
 // ---------------------------------------------------------------------------
 constexpr int R_CTAS = 8;          // cluster: the experts are split over its CTAs
-constexpr int R_THREADS = 256;
+constexpr int R_WARPS = 8;         // warps for the logits; four more quantise x meanwhile
+constexpr int R_THREADS = 32 * (R_WARPS + 4);
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
@@ -57,66 +58,81 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
-// One cluster per TG tokens.  Each warp takes two experts at a time over the
-// whole width (the lanes split it, 16 bytes each); the logits of token i go to
-// the shared memory of the cluster's CTA i, whose first warp selects.
+// One cluster per TG tokens.  A warp takes two experts at a time over a range
+// of the width (its lanes split it, 16 bytes each; the width is split where
+// there are fewer pairs of experts than warps); the sums of token i go to the
+// shared memory of the cluster's CTA i, whose first warp adds the ranges in
+// order and selects.
 template <int TG>
 __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_constant__ MoeArgs a) {
+  __shared__ float part[R_WARPS][kMoeMaxE];
   __shared__ float logits[kMoeMaxE];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int t0 = static_cast<int>(blockIdx.x / R_CTAS) * TG;
   const int nt = a.T - t0 < TG ? a.T - t0 : TG;
+  const int epc = (a.E + R_CTAS - 1) / R_CTAS;               // experts per CTA
+  const int pairs = (epc + 1) / 2;
+  const int splits = pairs > 4 ? 1 : pairs > 2 ? 2 : pairs > 1 ? 4 : 8;
   pdl_wait();
   pdl_launch_dependents();
-  for (int i = blockIdx.x * R_THREADS + threadIdx.x; i < a.ncounters; i += gridDim.x * R_THREADS)
-    a.counters[i] = 0;
   cluster_sync_all();          // the other CTAs' shared memory exists
 
-  const int epc = (a.E + R_CTAS - 1) / R_CTAS;
-  const int e_end = (rank + 1) * epc < a.E ? (rank + 1) * epc : a.E;
-  for (int e0 = rank * epc + 2 * warp; e0 < e_end; e0 += 2 * (R_THREADS / 32)) {
-    const bool two = e0 + 1 < e_end;
-    const __nv_bfloat16* r0 = a.router + static_cast<int64_t>(e0) * a.d;
-    const __nv_bfloat16* r1 = two ? r0 + a.d : r0;
-    float acc[2][TG];
+  if (warp >= R_WARPS) {
+    // counters of the next kernel, and x: one half-warp per block of 128 columns
+    const int tid = threadIdx.x - 32 * R_WARPS;
+    for (int i = blockIdx.x * 128 + tid; i < a.ncounters; i += gridDim.x * 128) a.counters[i] = 0;
+    const int nb = (a.d + kFp8Block - 1) / kFp8Block;
+    const int odd = (tid >> 4) & 1;
+    for (int kb = rank * 8 + (tid >> 4); kb - odd < nb; kb += R_CTAS * 8)
+      fp8_quant_rows4(a.X, a.T, a.d, a.ldx, a.xq, a.xs, a.ld_x, t0, kb);
+  } else {
+    const int e_end = (rank + 1) * epc < a.E ? (rank + 1) * epc : a.E;
+    const int split = warp % splits;
+    const int steps = (a.d + 255) / 256;                     // 256 columns each
+    const int c_lo = 256 * (steps * split / splits), c_hi = 256 * (steps * (split + 1) / splits);
+    const int c_end = c_hi < a.d ? c_hi : a.d;
+    for (int e0 = rank * epc + 2 * (warp / splits); e0 < e_end; e0 += 2 * (R_WARPS / splits)) {
+      const bool two = e0 + 1 < e_end;
+      const __nv_bfloat16* r0 = a.router + static_cast<int64_t>(e0) * a.d;
+      const __nv_bfloat16* r1 = two ? r0 + a.d : r0;
+      float acc[2][TG];
 #pragma unroll
-    for (int i = 0; i < TG; ++i) acc[0][i] = acc[1][i] = 0.f;
+      for (int i = 0; i < TG; ++i) acc[0][i] = acc[1][i] = 0.f;
 #pragma unroll 4
-    for (int c = 8 * lane; c < a.d; c += 256) {
-      const uint4 w0 = *reinterpret_cast<const uint4*>(r0 + c);
-      const uint4 w1 = *reinterpret_cast<const uint4*>(r1 + c);
+      for (int c = c_lo + 8 * lane; c < c_end; c += 256) {
+        const uint4 w0 = *reinterpret_cast<const uint4*>(r0 + c);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(r1 + c);
+#pragma unroll
+        for (int i = 0; i < TG; ++i) {
+          const int t = i < nt ? t0 + i : t0;
+          const uint4 x = *reinterpret_cast<const uint4*>(a.X + t * a.ldx + c);
+          acc[0][i] += dot8(x, w0);
+          acc[1][i] += dot8(x, w1);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < TG; ++i) {
-        const int t = i < nt ? t0 + i : t0;
-        const uint4 x = *reinterpret_cast<const uint4*>(a.X + t * a.ldx + c);
-        acc[0][i] += dot8(x, w0);
-        acc[1][i] += dot8(x, w1);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          acc[0][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][i], o);
+          acc[1][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[1][i], o);
+        }
+        if (lane == 0 && i < nt) {
+          st_cluster_f32(mapa_shared(smem_u32(&part[split][e0]), i), acc[0][i]);
+          if (two) st_cluster_f32(mapa_shared(smem_u32(&part[split][e0 + 1]), i), acc[1][i]);
+        }
       }
     }
-#pragma unroll
-    for (int i = 0; i < TG; ++i) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        acc[0][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][i], o);
-        acc[1][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[1][i], o);
-      }
-      if (lane == 0 && i < nt) {
-        st_cluster_f32(mapa_shared(smem_u32(&logits[e0]), i), acc[0][i]);
-        if (two) st_cluster_f32(mapa_shared(smem_u32(&logits[e0 + 1]), i), acc[1][i]);
-      }
-    }
-  }
-  // x of these tokens: one half-warp per block of 128 columns
-  {
-    const int nb = (a.d + kFp8Block - 1) / kFp8Block;
-    const int h = rank * (R_THREADS / 16) + static_cast<int>(threadIdx.x >> 4);
-    for (int kb = h; kb - static_cast<int>((threadIdx.x >> 4) & 1) < nb; kb += R_CTAS * (R_THREADS / 16))
-      for (int t = t0; t < t0 + nt; t += 4)
-        fp8_quant_rows4(a.X, TG >= 4 ? a.T : t0 + nt, a.d, a.ldx, a.xq, a.xs, a.ld_x, t, kb);
   }
   cluster_sync_all();
   if (warp != 0 || rank >= nt) return;
+  for (int e = lane; e < a.E; e += 32) {
+    float l = part[0][e];
+    for (int s = 1; s < splits; ++s) l += part[s][e];
+    logits[e] = l;
+  }
+  __syncwarp();
 
   // Selection of token t0 + rank.  Keys order as the logits do; NaN comes last
   // (key 1) and what has been taken is 0.
@@ -140,7 +156,7 @@ __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_const
     int bi = 0;
 #pragma unroll
     for (int i = 0; i < kMoeMaxE / 32; ++i)
-      if (key[i] > best) {               // the first of equal keys: the lower index
+      if (32 * i < a.E && key[i] > best) {   // the first of equal keys: the lower index
         best = key[i];
         bi = i;
       }
@@ -178,11 +194,12 @@ __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_const
 // Experts
 // ---------------------------------------------------------------------------
 // How many ranges K is split into: the fewest steps of the longest CTA, a unit
-// counted as its K blocks and two more for its start and end.
-__host__ __device__ inline int moe_split(int units, int nkb, int most, int ctas) {
+// counted as its K blocks and two more for its start and end, and `join` more
+// where it is split.
+__host__ __device__ inline int moe_split(int units, int nkb, int most, int ctas, int join) {
   int best = 1, cost = 0x7FFFFFFF;
   for (int s = 1; s <= most && s <= nkb; ++s) {
-    const int c = ((units * s + ctas - 1) / ctas) * ((nkb + s - 1) / s + 2);
+    const int c = ((units * s + ctas - 1) / ctas) * ((nkb + s - 1) / s + 2 + (s > 1 ? join : 0));
     if (c < cost) {
       cost = c;
       best = s;
@@ -191,10 +208,10 @@ __host__ __device__ inline int moe_split(int units, int nkb, int most, int ctas)
   return best;
 }
 
-constexpr int M_THREADS = 256;     // weights, MMA, activations, idle, 4 epilogue warps
+constexpr int M_THREADS = 384;     // weights, MMA, activations, idle, 4 epilogue, 4 finishing warps
 constexpr int M_W_BYTES = 2 * 128 * 128;
 constexpr int M_UNITS = 4;         // units between the producer and the epilogue
-constexpr int M_CONSUMERS = 6;     // warps that read a unit: MMA, activations, epilogue
+constexpr int M_CONSUMERS = 10;    // warps that read a unit: all but weights and idle
 
 struct MoeUnit {
   int kind;          // 0: up, 1: down, 2: no more
@@ -206,9 +223,10 @@ struct MoeUnit {
 template <int N>
 struct MoeSmem {
   static constexpr int kStageBytes = M_W_BYTES + N * 128;
-  static constexpr int kStages = N == 16 ? 6 : 5;
+  static constexpr int kStages = N == 64 ? 3 : 5;
   static constexpr int kSaSlots = kStages + 2;      // as in the few-token product
   uint8_t stage[kStages][kStageBytes];
+  float sums[N][256];                               // a unit's sums, by pair and tile row
   alignas(16) float sa[kSaSlots][N];
   float2 sb[kSaSlots];                              // scales of the two weight tiles
   uint64_t mask[kMoeMaxE];                          // tokens of each expert
@@ -224,6 +242,8 @@ struct MoeSmem {
   uint64_t sa_full[kSaSlots];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t sums_full;
+  uint64_t sums_empty;
   uint64_t drain;
   int n_act, s_up, s_dn;
   int last;
@@ -281,28 +301,53 @@ __device__ __forceinline__ float moe_gelu(float y) {
   return y / (1.0f + expf(-2.0f * u));
 }
 
+// After all 128 finishing threads' writes: counts one arrival; true for all of
+// them if it was the last of `all`, whose earlier writes they may then read.
+__device__ __forceinline__ bool moe_last_arrival(int* counter, int all, int* last, int tid) {
+  named_bar_sync(1, 128);
+  if (tid == 0) {
+    __threadfence();
+    *last = atomicAdd(counter, 1) == all - 1;
+    __threadfence();
+  }
+  named_bar_sync(1, 128);
+  return *last != 0;
+}
+
 // One block of 128 hidden rows of one expert, all its pairs, by the 128
-// epilogue threads: the ranges' sums joined in order, the activation, and the
-// e4m3 codes with their scale.
+// finishing threads: the activation and the e4m3 codes with their scale.  The
+// sums are this CTA's own in shared memory (`own`, rows at `second` where there
+// is no gate), or, with K split, the ranges' in the workspace, added in order.
 template <bool kGated>
 __device__ __forceinline__ void moe_finish_h(const MoeArgs& a, uint32_t (&amax)[2][4][4], int off, int m,
-                                             int blk, int splits, int tid) {
+                                             int blk, int splits, const float* own, int second, int tid) {
   const int row = blk * 128 + tid;
   const bool in = row < a.ff;
   const int64_t stride = static_cast<int64_t>(kGated ? 2 : 1) * a.ff;      // floats per pair
   int buf = 0;
   for (int p0 = 0; p0 < m; p0 += 4, buf ^= 1) {
     float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s) {
-      const float* ps = a.part_up + (static_cast<int64_t>(s) * a.pairs + off + p0) * stride + row;
+    if (own != nullptr) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (in && p0 + i < m) {
-          if constexpr (kGated) {
-            g[i] += __ldcg(ps + i * stride);
-            u[i] += __ldcg(ps + i * stride + a.ff);
-          } else {
-            u[i] += __ldcg(ps + i * stride);
+          g[i] = own[(p0 + i) * 256];
+          u[i] = kGated ? own[(p0 + i) * 256 + 128] : own[(p0 + i) * 256 + second];
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int s = 0; s < splits; ++s) {
+        const float* ps = a.part_up + (static_cast<int64_t>(s) * a.pairs + off + p0) * stride + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (in && p0 + i < m) {
+            if constexpr (kGated) {
+              g[i] += __ldcg(ps + i * stride);
+              u[i] += __ldcg(ps + i * stride + a.ff);
+            } else {
+              u[i] += __ldcg(ps + i * stride);
+            }
           }
         }
       }
@@ -328,6 +373,50 @@ __device__ __forceinline__ void moe_finish_h(const MoeArgs& a, uint32_t (&amax)[
         if (tid == 0) a.hs[static_cast<int64_t>(blk) * a.pairs + r] = f8_scale(eb);
       }
     }
+  }
+}
+
+// y: the weighted sum of the chosen experts' outputs, in the order of selection,
+// over the ranges of K in order.  Thread i of `threads` over the whole grid takes
+// every `threads`-th pair of columns.
+__device__ __forceinline__ void moe_combine(const MoeArgs& a, const uint16_t* row_of, int splits, int i,
+                                            int threads) {
+  const int half = a.d / 2;
+  const int64_t range = a.pairs * a.d;
+  for (; i < a.T * half; i += threads) {
+    const int t = i / half, col = 2 * (i - t * half);
+    float2 y = make_float2(0.f, 0.f);
+    for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+      float2 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = make_float2(0.f, 0.f);
+#pragma unroll 2
+      for (int s = 0; s < splits; ++s) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j0 + j < a.top_k) {
+            const int64_t r = row_of[t * a.top_k + j0 + j];
+            const float2 w = __ldcg(reinterpret_cast<const float2*>(a.part_dn + s * range + r * a.d + col));
+            v[j].x += w.x;
+            v[j].y += w.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j0 + j < a.top_k) {
+          const float wt = a.wts[t * a.top_k + j0 + j];
+          y.x = fmaf(wt, v[j].x, y.x);
+          y.y = fmaf(wt, v[j].y, y.y);
+        }
+      }
+    }
+    const int64_t at = t * a.ldy + col;
+    if (a.y_f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + at) = y;
+    else
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.Y) + at) =
+          __floats2bfloat162_rn(y.x, y.y);
   }
 }
 
@@ -364,6 +453,8 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       mbar_init(&sm.unit_full[u], 1);
       mbar_init(&sm.unit_empty[u], M_CONSUMERS);
     }
+    mbar_init(&sm.sums_full, 4);
+    mbar_init(&sm.sums_empty, 4);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0u;
     fence_barrier_init();
@@ -389,6 +480,8 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   // most), the experts that have any in ascending order, and the rows of their
   // (token, expert) pairs: expert by expert, tokens ascending, each expert's
   // first row a multiple of 4 so that its scales start on 16 bytes.
+  int first_unit = 0;
+  if (threadIdx.x == 0) first_unit = atomicAdd(a.ticket, 1);
   const int npairs = a.T * a.top_k;
   for (int p = threadIdx.x; p < npairs; p += M_THREADS)
     atomicOr(reinterpret_cast<unsigned long long*>(&sm.mask[a.ids[p]]), 1ull << (p / a.top_k));
@@ -415,8 +508,8 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     }
     if (lane == 0) {
       sm.n_act = n;
-      sm.s_up = moe_split(n * up_units, nkb_d, a.most_up, static_cast<int>(gridDim.x));
-      sm.s_dn = moe_split(n * dn_tiles, nkb_f, a.most_dn, static_cast<int>(gridDim.x));
+      sm.s_up = moe_split(n * up_units, nkb_d, a.most_up, static_cast<int>(gridDim.x), 6);
+      sm.s_dn = moe_split(n * dn_tiles, nkb_f, a.most_dn, static_cast<int>(gridDim.x), 0);
     }
   }
   __syncthreads();
@@ -432,9 +525,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
 
   if (warp == 0) {
     // ================== weights (and the order of the units) ==============
-    int next = 0;
-    if (lane == 0) next = atomicAdd(a.ticket, 1);
-    next = __shfl_sync(0xFFFFFFFFu, next, 0);
+    int next = __shfl_sync(0xFFFFFFFFu, first_unit, 0);
     uint32_t it = 0, u = 0;
     bool ok = true;
     while (ok) {
@@ -605,34 +696,30 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     __syncwarp();
     mbar_wait_bounded(&sm.drain, 0u, nullptr, DEVERR_TIMEOUT_MMA);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     // ============================ epilogue ================================
-    // The four warps agree at every barrier on whether one of them gave up
-    // (named_bar_or), so none is left waiting for another.
+    // Adds the K blocks' partial sums in registers and hands a unit's sums on.
     const int sp = warp & 3;
     const int tid = 32 * sp + lane;                    // the tile row of this thread
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
     uint32_t it = 0;
-    for (uint32_t u = 0;; ++u) {
+    bool ok = true;
+    for (uint32_t u = 0; ok; ++u) {
       const int us = static_cast<int>(u % M_UNITS);
-      bool ok = warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag,
-                                  DEVERR_TIMEOUT_EPILOGUE);
-      if (named_bar_or(1, 128, !ok)) break;
+      if (!warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
+        break;
       const MoeUnit un = sm.unit[us];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.unit_empty[us]);
       if (un.kind == 2) break;
-      const int e = sm.act_e[un.ex];
-      const int off = sm.off[e];
-      const uint64_t mk = sm.mask[e];
-      const int m = __popcll(mk);
+      const uint64_t mk = sm.mask[sm.act_e[un.ex]];
       const int nkb = un.kind == 0 ? nkb_d : nkb_f;
       const int splits = un.kind == 0 ? s_up : s_dn;
-      const int k0 = kb_lo(nkb, un.split, splits), k1 = kb_lo(nkb, un.split + 1, splits);
+      const int nk = kb_lo(nkb, un.split + 1, splits) - kb_lo(nkb, un.split, splits);
       float2 acc[2][N / 2];
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) acc[0][j] = acc[1][j] = make_float2(0.f, 0.f);
-      for (int kb = k0; kb < k1; ++kb, ++it) {
+      for (int i = 0; i < nk; ++i, ++it) {
         const int q = static_cast<int>(it % Smem::kSaSlots);
         const uint32_t b = it & 1u;
         if (!warp_wait_bounded(&sm.sa_full[q], (it / Smem::kSaSlots) & 1u, abort_flag,
@@ -650,7 +737,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
           for (int c = 0; c < N / 16; ++c) {
             uint32_t r[16];
             tmem_ld_32x32b_x16(taddr + b * 2 * N + h * N + 16 * c, r);
-            tmem_ld_wait();
+            tmem_ld_wait_for(r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][16 * c + 4 * j]);
@@ -667,90 +754,106 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
       }
-      if (named_bar_or(1, 128, !ok)) break;
-      // this unit's sums, pair by pair
-      if (un.kind == 0) {
-        const int r0 = (kGated ? un.blk : 2 * un.blk) * 128 + tid;
-        const int64_t stride = static_cast<int64_t>(kGated ? 2 : 1) * a.ff;
-        float* p = a.part_up + (static_cast<int64_t>(un.split) * a.pairs + off) * stride + r0;
-        const bool in0 = r0 < a.ff, in1 = kGated ? in0 : r0 + 128 < a.ff;
-        const int64_t second_at = kGated ? a.ff : 128;
+      if (!ok || !warp_wait_bounded(&sm.sums_empty, (u & 1u) ^ 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
+        break;
+      // up: the columns are all tokens, those of this expert are kept; down: the
+      // columns are the expert's pairs, then others'
+      const uint64_t keep = un.kind == 0 ? mk : ~0ull >> (64 - __popcll(mk));
+      float* p = &sm.sums[0][tid];
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-          if ((mk >> c) & 1ull) {
-            if (in0) __stcg(p, (c & 1) ? acc[0][c >> 1].y : acc[0][c >> 1].x);
-            if (in1) __stcg(p + second_at, (c & 1) ? acc[1][c >> 1].y : acc[1][c >> 1].x);
-            p += stride;
+      for (int c = 0; c < N; ++c) {
+        if ((keep >> c) & 1ull) {
+          p[0] = (c & 1) ? acc[0][c >> 1].y : acc[0][c >> 1].x;
+          p[128] = (c & 1) ? acc[1][c >> 1].y : acc[1][c >> 1].x;
+          p += 256;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.sums_full);
+    }
+  } else if (warp >= 8) {
+    // ============================ finishing ===============================
+    // What follows a unit's sums, while the next unit's are made.  The four
+    // warps agree at their barriers on whether one of them gave up
+    // (named_bar_or), so none is left waiting for another.
+    const int tid = threadIdx.x - 256;
+    for (uint32_t u = 0;; ++u) {
+      const int us = static_cast<int>(u % M_UNITS);
+      bool ok = warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag,
+                                  DEVERR_TIMEOUT_EPILOGUE);
+      if (named_bar_or(1, 128, !ok)) break;
+      const MoeUnit un = sm.unit[us];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[us]);
+      if (un.kind == 2) break;
+      ok = warp_wait_bounded(&sm.sums_full, u & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+      if (named_bar_or(1, 128, !ok)) break;
+      const int e = sm.act_e[un.ex];
+      const int off = sm.off[e];
+      const int m = __popcll(sm.mask[e]);
+      const float* own = &sm.sums[0][tid];
+      if (un.kind == 0) {
+        bool finish = true;
+        if (s_up > 1) {
+          // this range's sums to the workspace; the last range to arrive goes on
+          const int r0 = (kGated ? un.blk : 2 * un.blk) * 128 + tid;
+          const int64_t stride = static_cast<int64_t>(kGated ? 2 : 1) * a.ff;
+          const int64_t second_at = kGated ? a.ff : 128;
+          const bool in0 = r0 < a.ff, in1 = kGated ? in0 : r0 + 128 < a.ff;
+          float* p = a.part_up + (static_cast<int64_t>(un.split) * a.pairs + off) * stride + r0;
+          for (int i = 0; i < m; ++i, p += stride) {
+            if (in0) __stcg(p, own[i * 256]);
+            if (in1) __stcg(p + second_at, own[i * 256 + 128]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sums_empty);
+          finish = moe_last_arrival(a.up_done + un.ex * up_units + un.blk, s_up, &sm.last, tid);
+        }
+        if (finish) {
+          const float* src = s_up > 1 ? nullptr : own;
+          if constexpr (kGated) {
+            moe_finish_h<true>(a, sm.amax, off, m, un.blk, s_up, src, 0, tid);
+          } else {
+            moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk, s_up, src, 0, tid);
+            named_bar_sync(1, 128);
+            if (2 * un.blk + 1 < nkb_f)
+              moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk + 1, s_up, src, 128, tid);
+          }
+          if (s_up == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.sums_empty);
+          }
+          fence_proxy_async_global();
+          named_bar_sync(1, 128);
+          if (tid == 0) {
+            __threadfence();
+            atomicAdd(a.ready + un.ex, 1);
           }
         }
       } else {
         const int r0 = un.blk * 256 + tid;
-        float* p = a.part_dn + (static_cast<int64_t>(un.split) * a.pairs + off) * a.d + r0;
         const bool in0 = r0 < a.d, in1 = r0 + 128 < a.d;
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-          if (c < m) {
-            if (in0) __stcg(p, (c & 1) ? acc[0][c >> 1].y : acc[0][c >> 1].x);
-            if (in1) __stcg(p + 128, (c & 1) ? acc[1][c >> 1].y : acc[1][c >> 1].x);
-            p += a.d;
-          }
+        float* p = a.part_dn + (static_cast<int64_t>(un.split) * a.pairs + off) * a.d + r0;
+        for (int i = 0; i < m; ++i, p += a.d) {
+          if (in0) __stcg(p, own[i * 256]);
+          if (in1) __stcg(p + 128, own[i * 256 + 128]);
         }
-      }
-      // the last of the units that make up a block finishes it
-      __threadfence();
-      named_bar_sync(1, 128);
-      if (tid == 0) {
-        int* ctr = un.kind == 0 ? a.up_done + un.ex * up_units + un.blk : a.dn_done + un.blk;
-        const int all = un.kind == 0 ? s_up : n_act * s_dn;
-        sm.last = atomicAdd(ctr, 1) == all - 1;
-        __threadfence();
-      }
-      named_bar_sync(1, 128);
-      if (!sm.last) continue;
-      if (un.kind == 0) {
-        if constexpr (kGated) {
-          moe_finish_h<true>(a, sm.amax, off, m, un.blk, s_up, tid);
-        } else {
-          moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk, s_up, tid);
-          named_bar_sync(1, 128);
-          if (2 * un.blk + 1 < nkb_f) moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk + 1, s_up, tid);
-        }
-        fence_proxy_async_global();
-        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sums_empty);
         named_bar_sync(1, 128);
         if (tid == 0) {
           __threadfence();
-          atomicAdd(a.ready + un.ex, 1);
-        }
-      } else {
-        const int col = un.blk * 256 + 2 * tid;
-        if (col < a.d) {
-          for (int t = 0; t < a.T; ++t) {
-            float2 y = make_float2(0.f, 0.f);
-#pragma unroll 4
-            for (int j = 0; j < a.top_k; ++j) {
-              const int pr = t * a.top_k + j;
-              const float* p = a.part_dn + static_cast<int64_t>(sm.row_of[pr]) * a.d + col;
-              float2 v = __ldcg(reinterpret_cast<const float2*>(p));
-              for (int s = 1; s < s_dn; ++s) {
-                const float2 w = __ldcg(reinterpret_cast<const float2*>(p + s * a.pairs * a.d));
-                v.x += w.x;
-                v.y += w.y;
-              }
-              const float wt = a.wts[pr];
-              y.x = fmaf(wt, v.x, y.x);
-              y.y = fmaf(wt, v.y, y.y);
-            }
-            const int64_t at = t * a.ldy + col;
-            if (a.y_f32)
-              *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + at) = y;
-            else
-              *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.Y) + at) =
-                  __floats2bfloat162_rn(y.x, y.y);
-          }
+          atomicAdd(a.dn_done, 1);
         }
       }
     }
+    // y, once all down units are done: every CTA a share.  (Like the wait for h,
+    // this one is for units that running CTAs have taken.)
+    bool done = *abort_flag == 0u;
+    if (done && tid == 0)
+      done = counter_wait_bounded(a.dn_done, dn_tiles * n_act * s_dn, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+    if (!named_bar_or(1, 128, !done))
+      moe_combine(a, sm.row_of, s_dn, blockIdx.x * 128 + tid, gridDim.x * 128);
   }
 
   tc_fence_before();
@@ -799,7 +902,7 @@ MoeLayout moe_layout(int64_t T, int64_t d, int64_t ff, int64_t E, int64_t top_k,
   l.up_done = 0;
   l.ready = l.up_done + nE * up_units;
   l.dn_done = l.ready + nE;
-  l.ticket = l.dn_done + dn_tiles;
+  l.ticket = l.dn_done + 1;
   l.ncounters = l.ticket + 1;
   size_t at = 0;
   auto take = [&](int64_t bytes) {
