@@ -381,10 +381,7 @@ w4a4_status w4a4_fp8_gemm(const uint8_t* a, const float* scale_a, int64_t ld_sca
 /* Bytes of device workspace w4a4_fp8_linear needs for T tokens of d_in columns. */
 w4a4_status w4a4_fp8_workspace_size(int64_t T, int64_t d_in, size_t* bytes);
 
-/* The layer: w4a4_fp8_quant_act into the workspace, then w4a4_fp8_gemm.  The
- * weight must not be written by work still running on other streams (as for
- * any call), and may be read before the kernel just before this call's own
- * second one has ended. */
+/* The layer: w4a4_fp8_quant_act into the workspace, then w4a4_fp8_gemm. */
 w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp8_weight* w,
                             void* workspace, size_t ws_bytes, void* Y, int64_t ldy, int y_f32,
                             void* stream);

@@ -114,7 +114,7 @@ w4a4_status w4a4_fp8_gemm(const uint8_t* a, const float* scale_a, int64_t ld_sca
   if (st != W4A4_OK || T == 0) return st;
   Fp8GemmPlan p;
   cudaError_t e = plan_fp8_gemm(a, scale_a, ld_scale, T, w->d_in, w->d_out, w->q, w->scale, Y, ldy,
-                                y_f32 != 0, false, &p);
+                                y_f32 != 0, &p);
   if (e == cudaSuccess) e = run_fp8_gemm(p, static_cast<cudaStream_t>(stream));
   return from_cuda(e);
 }
@@ -147,7 +147,7 @@ w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp
   if (st != W4A4_OK) return st;
   Fp8GemmPlan p;
   cudaError_t e = plan_fp8_gemm(q, scale, ws.ld_scale, T, w->d_in, w->d_out, w->q, w->scale, Y, ldy,
-                                y_f32 != 0, pdl_enabled(), &p);
+                                y_f32 != 0, &p);
   if (e != cudaSuccess) return W4A4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   e = launch_fp8_quant_act(X, T, w->d_in, ldx, q, scale, ws.ld_scale, s);

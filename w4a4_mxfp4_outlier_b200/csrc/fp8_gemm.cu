@@ -15,7 +15,7 @@
 //    per tile, persistent.
 //  * fp8_gemm_few_kernel: for few tokens, where reading the weight is the
 //    work: the weight rows are the MMA's M (128 per CTA), the tokens its N
-//    (16 .. 128), and the CTAs of a cluster split K and join their sums through
+//    (16 .. 64), and the CTAs of a cluster split K and join their sums through
 //    distributed shared memory, in the order of the ranks.
 // Every wait is bounded, as in the other kernels of the library.
 #include <cuda.h>
@@ -28,32 +28,35 @@ namespace w4a4 {
 // ---------------------------------------------------------------------------
 // few tokens
 // ---------------------------------------------------------------------------
-constexpr int F_THREADS = 192;                // producer, MMA, 4 epilogue warps
+constexpr int F_THREADS = 224;                // weights, MMA, 4 epilogue, activations
 constexpr int F_W_BYTES = 128 * 128;          // weight rows x bytes of one K block
+constexpr int F_BUFS = 4;                     // accumulators in tensor memory
 
 template <int N>
 struct FewSmem {
-  // about 96 KB in flight per CTA, two CTAs per SM
+  // about 90 KB in flight, two CTAs per SM (so that the next kernel's are
+  // already there when this one's leave; 1 token, 5120 -> 13824: 16.8 us, with
+  // one CTA of 195 KB per SM 19.3)
   static constexpr int kStageBytes = F_W_BYTES + N * 128;
-  static constexpr int kStages = N <= 32 ? 5 : (N == 64 ? 4 : 3);
-  // An accumulator buffer is reused two K blocks later, after the epilogue has
-  // read the scales of the first, so two slots more than stages are enough.
-  static constexpr int kSaSlots = kStages + 2;
+  static constexpr int kStages = N <= 32 ? 5 : 4;
+  // An accumulator buffer is reused F_BUFS K blocks later, after the epilogue
+  // has read the scales of the first, so F_BUFS slots more than stages are enough.
+  static constexpr int kSaSlots = kStages + F_BUFS;
   uint8_t stage[kStages][kStageBytes];
   alignas(16) float sa[kSaSlots][N];
   float sb[kSaSlots];
   uint64_t full[kStages];
   uint64_t empty[kStages];
   uint64_t sa_full[kSaSlots];
-  uint64_t acc_full[2];
-  uint64_t acc_empty[2];
+  uint64_t acc_full[F_BUFS];
+  uint64_t acc_empty[F_BUFS];
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t abort_flag;
   static_assert(N * 512 <= kStages * kStageBytes, "the sums fit the ring");
 };
 
-template <int N, bool kF32>
+template <int N>
 __global__ void __launch_bounds__(F_THREADS, 2)
     fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w,
                         const __grid_constant__ CUtensorMap tm_x,
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(F_THREADS, 2)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   using Smem = FewSmem<N>;
   constexpr int NST = Smem::kStages;
-  constexpr int TCOLS = 2 * N < 32 ? 32 : 2 * N;
+  constexpr int TCOLS = F_BUFS * N;
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   volatile uint32_t* abort_flag = &sm.abort_flag;
@@ -70,19 +73,18 @@ __global__ void __launch_bounds__(F_THREADS, 2)
   const int C = static_cast<int>(gridDim.z);              // cluster = CTAs along z, one K range each
   const int rank = static_cast<int>(blockIdx.z);
   const int n0 = blockIdx.x * 128;
-  const int t0 = blockIdx.y * N;
-  const int nt = args.T - t0 < N ? args.T - t0 : N;       // tokens of this tile
+  const int nt = args.T;                                  // at most N
   const int kb0 = static_cast<int>(static_cast<int64_t>(args.nkb) * rank / C);
   const int kb1 = static_cast<int>(static_cast<int64_t>(args.nkb) * (rank + 1) / C);
   const int nk = kb1 - kb0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.full[s], 2);                       // weights, activations
       mbar_init(&sm.empty[s], 1);
     }
     for (int s = 0; s < Smem::kSaSlots; ++s) mbar_init(&sm.sa_full[s], 1);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < F_BUFS; ++b) {
       mbar_init(&sm.acc_full[b], 1);
       mbar_init(&sm.acc_empty[b], 4);
     }
@@ -101,24 +103,31 @@ __global__ void __launch_bounds__(F_THREADS, 2)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
+  pdl_wait();
+  pdl_launch_dependents();
+
   if (warp == 0) {
-    // ============================ TMA producer ============================
-    // In w4a4_fp8_linear the previous kernel is the library's quantiser, which
-    // lets this one start only after everything before it has ended, and which
-    // does not write the weight: the first weight tiles are then fetched
-    // before waiting for it.
-    const uint32_t sa_bytes = static_cast<uint32_t>((nt + 3) & ~3) * 4u;
-    const int early = args.early_weights ? (nk < NST ? nk : NST) : 0;
-    if (elect_one()) {
-      for (int i = 0; i < early; ++i) {
-        mbar_arrive_expect_tx(&sm.full[i], Smem::kStageBytes);
-        tma_load_2d(sm.stage[i], &tm_w, &sm.full[i], (kb0 + i) * 128, n0);
-      }
-    }
-    __syncwarp();
-    pdl_wait();
-    pdl_launch_dependents();
+    // ============================ weights =================================
     uint32_t issued = 0;
+    for (int i = 0; i < nk; ++i) {
+      const int s = i % NST;
+      if (i >= NST && !warp_wait_bounded(&sm.empty[s], ((i / NST) & 1) ^ 1u, abort_flag,
+                                         DEVERR_TIMEOUT_PRODUCER))
+        break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sm.full[s], F_W_BYTES);
+        tma_load_2d(sm.stage[s], &tm_w, &sm.full[s], (kb0 + i) * 128, n0);
+      }
+      __syncwarp();
+      issued = i + 1;
+    }
+    if (issued != 0 && *abort_flag) spin_ns(200000);   // copies in flight land before teardown
+    __syncwarp();
+  } else if (warp == 6) {
+    // ============================ activations =============================
+    // (a warp of its own: one warp's copies for weights and activations take
+    // some 500 cycles a K block to issue)
+    const uint32_t sa_bytes = static_cast<uint32_t>((nt + 3) & ~3) * 4u;
     WarpRun sb(args.sb + static_cast<int64_t>(blockIdx.x) * args.nkb + kb0, nk);
     for (int i = 0; i < nk; ++i) {
       const int s = i % NST;
@@ -128,37 +137,24 @@ __global__ void __launch_bounds__(F_THREADS, 2)
                                          DEVERR_TIMEOUT_PRODUCER))
         break;
       if (elect_one()) {
-        if (i >= early) {
-          mbar_arrive_expect_tx(&sm.full[s], Smem::kStageBytes);
-          tma_load_2d(sm.stage[s], &tm_w, &sm.full[s], (kb0 + i) * 128, n0);
-        }
-        tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, t0);
+        mbar_arrive_expect_tx(&sm.full[s], N * 128);
+        tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, 0);
         sm.sb[q] = sbi;
         mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
-        bulk_load(sm.sa[q], args.sa + (kb0 + i) * args.ld_sa + t0, sa_bytes, &sm.sa_full[q]);
+        bulk_load(sm.sa[q], args.sa + (kb0 + i) * args.ld_sa, sa_bytes, &sm.sa_full[q]);
       }
       __syncwarp();
-      issued = i + 1;
     }
-    if (lane == 0 && *abort_flag) {
-      // wait for the copies still in flight, so none lands after teardown
-      const uint32_t first = issued > NST ? issued - NST : 0;
-      for (uint32_t i = first; i < issued; ++i) {
-        mbar_wait_bounded(&sm.full[i % NST], (i / NST) & 1u, nullptr, DEVERR_TIMEOUT_PRODUCER);
-        mbar_wait_bounded(&sm.sa_full[i % Smem::kSaSlots], (i / Smem::kSaSlots) & 1u, nullptr,
-                          DEVERR_TIMEOUT_PRODUCER);
-      }
-    }
+    if (*abort_flag) spin_ns(200000);
     __syncwarp();
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================
-    pdl_wait();
     const uint64_t dw0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]));
     const uint64_t dx0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]) + F_W_BYTES);
     for (int i = 0; i < nk; ++i) {
       const int s = i % NST;
-      const uint32_t b = i & 1;
-      if (!warp_wait_bounded(&sm.acc_empty[b], ((i >> 1) & 1) ^ 1u, abort_flag, DEVERR_TIMEOUT_MMA))
+      const uint32_t b = i % F_BUFS;
+      if (!warp_wait_bounded(&sm.acc_empty[b], ((i / F_BUFS) & 1) ^ 1u, abort_flag, DEVERR_TIMEOUT_MMA))
         break;
       if (!warp_wait_bounded(&sm.full[s], (i / NST) & 1u, abort_flag, DEVERR_TIMEOUT_MMA)) break;
       tc_fence_after();
@@ -178,7 +174,6 @@ __global__ void __launch_bounds__(F_THREADS, 2)
     __syncwarp();
   } else {
     // ============================ epilogue ================================
-    pdl_wait();
     const int sp = warp & 3;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
     float2 acc[N / 2];
@@ -186,10 +181,10 @@ __global__ void __launch_bounds__(F_THREADS, 2)
     for (int j = 0; j < N / 2; ++j) acc[j] = make_float2(0.f, 0.f);
     for (int i = 0; i < nk; ++i) {
       const int q = i % Smem::kSaSlots;
-      const uint32_t b = i & 1;
+      const uint32_t b = i % F_BUFS;
       if (!warp_wait_bounded(&sm.sa_full[q], (i / Smem::kSaSlots) & 1u, abort_flag,
                              DEVERR_TIMEOUT_EPILOGUE) ||
-          !warp_wait_bounded(&sm.acc_full[b], (i >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
+          !warp_wait_bounded(&sm.acc_full[b], (i / F_BUFS) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
         break;
       const float sb = sm.sb[q];
       tc_fence_after();
@@ -199,7 +194,7 @@ __global__ void __launch_bounds__(F_THREADS, 2)
         uint32_t r[CH];
         if constexpr (CH == 16) tmem_ld_32x32b_x16(taddr + b * N + c * CH, r);
         else tmem_ld_32x32b_x32(taddr + b * N + c * CH, r);
-        tmem_ld_wait();
+        tmem_ld_wait_for(r);
 #pragma unroll
         for (int j = 0; j < CH / 4; ++j) {
           const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][c * CH + 4 * j]);
@@ -242,21 +237,25 @@ __global__ void __launch_bounds__(F_THREADS, 2)
     for (int i = threadIdx.x; i < ((nt - rank + C - 1) / C) * 64; i += F_THREADS) {
       const int t = rank + (i >> 6) * C, c = 2 * (i & 63);
       if (n0 + c >= args.d_out) continue;                  // d_out is even
-      float2 v = make_float2(0.f, 0.f);
-      for (int r = 0; r < C; ++r) {
-        const float2 p = ld_cluster_f32x2(mapa_shared(red + 4u * (t * 128 + c), r));
-        v.x += p.x;
-        v.y += p.y;
+      float2 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        v[r] = r < C ? ld_cluster_f32x2(mapa_shared(red + 4u * (t * 128 + c), r)) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int r = 1; r < 8; ++r) {
+        v[0].x += v[r].x;
+        v[0].y += v[r].y;
       }
-      const int64_t at = (t0 + t) * args.ldy + n0 + c;
-      if constexpr (kF32) {
-        *reinterpret_cast<float2*>(static_cast<float*>(args.Y) + at) = v;
+      const int64_t at = t * args.ldy + n0 + c;
+      if (args.y_f32) {
+        *reinterpret_cast<float2*>(static_cast<float*>(args.Y) + at) = v[0];
       } else {
         *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(args.Y) + at) =
-            __floats2bfloat162_rn(v.x, v.y);
+            __floats2bfloat162_rn(v[0].x, v[0].y);
       }
     }
   }
+  __syncwarp();
   cluster_sync_all();          // no CTA leaves while another reads its sums
 }
 
@@ -597,12 +596,8 @@ static cudaError_t few_attr() {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-  const int bytes = static_cast<int>(sizeof(FewSmem<N>) + 1024);
-  e = cudaFuncSetAttribute(fp8_gemm_few_kernel<N, false>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fp8_gemm_few_kernel<N, true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(fp8_gemm_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(FewSmem<N>) + 1024));
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
   return e;
 }
@@ -638,11 +633,11 @@ static int fp8_pair_capacity() {
 }
 
 // Token counts up to this take the few-token kernel.
-constexpr int64_t kFp8FewMaxT = 512;
+constexpr int64_t kFp8FewMaxT = 64;
 
 cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int64_t T, int64_t d_in,
                           int64_t d_out, const uint8_t* wq, const float* wscale, void* Y, int64_t ldy,
-                          bool f32, bool early_weights, Fp8GemmPlan* p) {
+                          bool f32, Fp8GemmPlan* p) {
   memset(p, 0, sizeof(*p));
   p->empty = T == 0;
   if (p->empty) return cudaSuccess;
@@ -656,21 +651,23 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
   a.T = static_cast<int>(T);
   a.d_out = static_cast<int>(d_out);
   a.nkb = static_cast<int>((d_in + kFp8Block - 1) / kFp8Block);
-  a.early_weights = early_weights ? 1 : 0;
+  a.y_f32 = f32 ? 1 : 0;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (T <= kFp8FewMaxT) {
-    const int N = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-    cudaError_t e = N == 16 ? few_attr<16>() : N == 32 ? few_attr<32>() : N == 64 ? few_attr<64>() : few_attr<128>();
+    const int N = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    const cudaError_t e = N == 16 ? few_attr<16>() : N == 32 ? few_attr<32>() : few_attr<64>();
     if (e != cudaSuccess) return e;
     p->few = N;
-    p->smem = (N == 16 ? sizeof(FewSmem<16>) : N == 32 ? sizeof(FewSmem<32>)
-               : N == 64 ? sizeof(FewSmem<64>) : sizeof(FewSmem<128>)) + 1024;
-    const int tn = static_cast<int>((d_out + 127) / 128), tt = static_cast<int>((T + N - 1) / N);
-    // K is split while the tiles leave SMs without work (148 SMs, two CTAs each)
+    p->smem = (N == 16 ? sizeof(FewSmem<16>) : N == 32 ? sizeof(FewSmem<32>) : sizeof(FewSmem<64>)) + 1024;
+    const int tn = static_cast<int>((d_out + 127) / 128);
+    // K is split as far as all CTAs run at once, two per SM (sizes that pack
+    // into a GPU's groups of SMs; T = 1, 5120 -> 5120, 40 tiles: 1 16.2, 2 10.7,
+    // 3 9.0, 4 8.8, 6 8.2, 8 11.5 us)
     int C = 1;
-    while (C < 8 && 2 * C <= a.nkb && static_cast<int64_t>(tn) * tt * C < 120) C *= 2;
+    for (const int c : {2, 3, 4, 6, 8})
+      if (tn * c <= 2 * 148 && c <= a.nkb) C = c;
     p->cluster = C;
-    p->grid = dim3(tn, tt, C);
+    p->grid = dim3(tn, 1, C);
     if (!make_tmap(&p->tm_w, wq, u8, 1, d_in, d_out, d_in, 128) ||
         !make_tmap(&p->tm_x, aq, u8, 1, d_in, T, d_in, N))
       return cudaErrorInvalidValue;
@@ -710,11 +707,8 @@ cudaError_t run_fp8_gemm(const Fp8GemmPlan& p, cudaStream_t stream) {
   if (p.few) {
     cfg.blockDim = dim3(F_THREADS, 1, 1);
     attr[0].val.clusterDim.z = static_cast<unsigned>(p.cluster);
-    void (*k)(CUtensorMap, CUtensorMap, Fp8GemmArgs) = nullptr;
-    if (p.few == 16) k = p.f32 ? fp8_gemm_few_kernel<16, true> : fp8_gemm_few_kernel<16, false>;
-    else if (p.few == 32) k = p.f32 ? fp8_gemm_few_kernel<32, true> : fp8_gemm_few_kernel<32, false>;
-    else if (p.few == 64) k = p.f32 ? fp8_gemm_few_kernel<64, true> : fp8_gemm_few_kernel<64, false>;
-    else k = p.f32 ? fp8_gemm_few_kernel<128, true> : fp8_gemm_few_kernel<128, false>;
+    void (*k)(CUtensorMap, CUtensorMap, Fp8GemmArgs) =
+        p.few == 16 ? fp8_gemm_few_kernel<16> : p.few == 32 ? fp8_gemm_few_kernel<32> : fp8_gemm_few_kernel<64>;
     return cudaLaunchKernelEx(&cfg, k, p.tm_w, p.tm_x, p.a);
   }
   cfg.blockDim = dim3(Q_THREADS, 1, 1);

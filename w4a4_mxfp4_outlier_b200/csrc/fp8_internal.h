@@ -15,9 +15,8 @@ struct Fp8GemmArgs {
   const float* sb;          // [ceil(d_out / 128)][nkb]
   void* Y;
   int64_t ld_sa, ldy;
-  int T, d_out, nkb;
+  int T, d_out, nkb, y_f32;
   int tiles_m, tiles_n;     // pair kernel
-  int early_weights;        // weights may be read before the previous kernel has ended
 };
 
 // plan: tensor maps, tile choice (host only); run: the launch.
@@ -32,7 +31,7 @@ struct Fp8GemmPlan {
 };
 cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int64_t T, int64_t d_in,
                           int64_t d_out, const uint8_t* wq, const float* wscale, void* Y, int64_t ldy,
-                          bool f32, bool early_weights, Fp8GemmPlan* p);
+                          bool f32, Fp8GemmPlan* p);
 cudaError_t run_fp8_gemm(const Fp8GemmPlan& p, cudaStream_t stream);
 
 // The expert layer.  Pairs are (token, chosen expert), in rows sorted by expert.

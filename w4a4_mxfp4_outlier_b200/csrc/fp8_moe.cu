@@ -34,6 +34,9 @@ constexpr int kMoeMaxT = 64;
 constexpr int kMoeMaxE = 512;
 constexpr int kMoeMaxK = 16;
 constexpr int kMoeMaxSplit = 8;
+#ifndef MOE_JOIN
+#define MOE_JOIN 8
+#endif
 
 // ---------------------------------------------------------------------------
 // Router
@@ -193,23 +196,24 @@ __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // Experts
 // ---------------------------------------------------------------------------
-// How many ranges K is split into: the fewest steps of the longest CTA, a unit
-// counted as its K blocks and two more for its start and end, and `join` more
-// where it is split.
-__host__ __device__ inline int moe_split(int units, int nkb, int most, int ctas, int join) {
-  int best = 1, cost = 0x7FFFFFFF;
-  for (int s = 1; s <= most && s <= nkb; ++s) {
-    const int c = ((units * s + ctas - 1) / ctas) * ((nkb + s - 1) / s + 2 + (s > 1 ? join : 0));
-    if (c < cost) {
-      cost = c;
-      best = s;
-    }
-  }
-  return best;
+// How many ranges K is split into: the fewest K blocks for the CTA with the most
+// units, a unit counted as one more than its own, and `join` more where the
+// ranges have to be joined; split only for a gain of a tenth.  One warp, the
+// same result in all lanes.
+__device__ __forceinline__ int moe_split(int units, int nkb, int most, int ctas, int join) {
+  const int s = static_cast<int>(threadIdx.x & 31) + 1;
+  auto cost = [&](int n) {
+    return ((units * n + ctas - 1) / ctas) * ((nkb + n - 1) / n + 1) + (n > 1 ? join : 0);
+  };
+  const int c = s <= most && s <= nkb ? cost(s) : 0x3FFFFFF;
+  const uint32_t best = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(c) * 32u + s - 1);
+  const int c1 = __shfl_sync(0xFFFFFFFFu, c, 0);
+  return 10 * static_cast<int>(best >> 5) < 9 * c1 ? static_cast<int>(best & 31u) + 1 : 1;
 }
 
 constexpr int M_THREADS = 384;     // weights, MMA, activations, idle, 4 epilogue, 4 finishing warps
 constexpr int M_W_BYTES = 2 * 128 * 128;
+constexpr int M_BUFS = 4;          // pairs of accumulators in tensor memory
 constexpr int M_UNITS = 4;         // units between the producer and the epilogue
 constexpr int M_CONSUMERS = 10;    // warps that read a unit: all but weights and idle
 
@@ -224,7 +228,7 @@ template <int N>
 struct MoeSmem {
   static constexpr int kStageBytes = M_W_BYTES + N * 128;
   static constexpr int kStages = N == 64 ? 3 : 5;
-  static constexpr int kSaSlots = kStages + 2;      // as in the few-token product
+  static constexpr int kSaSlots = kStages + M_BUFS;      // as in the few-token product
   uint8_t stage[kStages][kStageBytes];
   float sums[N][256];                               // a unit's sums, by pair and tile row
   alignas(16) float sa[kSaSlots][N];
@@ -240,8 +244,8 @@ struct MoeSmem {
   uint64_t full[kStages];
   uint64_t empty[kStages];
   uint64_t sa_full[kSaSlots];
-  uint64_t acc_full[2];
-  uint64_t acc_empty[2];
+  uint64_t acc_full[M_BUFS];
+  uint64_t acc_empty[M_BUFS];
   uint64_t sums_full;
   uint64_t sums_empty;
   uint64_t drain;
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       mbar_init(&sm.empty[s], 1);
     }
     for (int s = 0; s < Smem::kSaSlots; ++s) mbar_init(&sm.sa_full[s], 1);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < M_BUFS; ++b) {
       mbar_init(&sm.acc_full[b], 1);
       mbar_init(&sm.acc_empty[b], 4);
     }
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     prefetch_tmap(&tm_hq);
   }
   if (warp == 1) {
-    tmem_alloc(&sm.tmem_base, 4 * N);
+    tmem_alloc(&sm.tmem_base, 2 * M_BUFS * N);
     tmem_relinquish();
   }
   for (int e = threadIdx.x; e < a.E; e += M_THREADS) sm.mask[e] = 0ull;
@@ -506,10 +510,12 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       n += __popc(any);
       rows += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
+    const int su = moe_split(n * up_units, nkb_d, a.most_up, static_cast<int>(gridDim.x), MOE_JOIN);
+    const int sd = moe_split(n * dn_tiles, nkb_f, a.most_dn, static_cast<int>(gridDim.x), 0);
     if (lane == 0) {
       sm.n_act = n;
-      sm.s_up = moe_split(n * up_units, nkb_d, a.most_up, static_cast<int>(gridDim.x), 6);
-      sm.s_dn = moe_split(n * dn_tiles, nkb_f, a.most_dn, static_cast<int>(gridDim.x), 0);
+      sm.s_up = su;
+      sm.s_dn = sd;
     }
   }
   __syncthreads();
@@ -632,7 +638,6 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       for (int kb = k0; kb < k1; ++kb, ++it) {
         const int s = static_cast<int>(it % NST);
         const int q = static_cast<int>(it % Smem::kSaSlots);
-        const float2 sb2 = make_float2(r0.get(kb - k0), r1.get(kb - k0));
         if (it >= NST && !warp_wait_bounded(&sm.empty[s], ((it / NST) & 1u) ^ 1u, abort_flag,
                                             DEVERR_TIMEOUT_PRODUCER)) {
           ok = false;
@@ -642,9 +647,13 @@ __global__ void __launch_bounds__(M_THREADS, 1)
           mbar_arrive_expect_tx(&sm.full[s], N * 128);
           tma_load_2d(sm.stage[s] + M_W_BYTES, un.kind == 0 ? &tm_xq : &tm_hq, &sm.full[s], kb * 128,
                       off);
+          bulk_load(sm.sa[q], sa + kb * ld, sa_bytes, &sm.sa_full[q]);
+        }
+        __syncwarp();
+        const float2 sb2 = make_float2(r0.get(kb - k0), r1.get(kb - k0));
+        if (elect_one()) {
           sm.sb[q] = sb2;
           mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
-          bulk_load(sm.sa[q], sa + kb * ld, sa_bytes, &sm.sa_full[q]);
         }
         __syncwarp();
       }
@@ -671,8 +680,8 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       const int nk = kb_lo(nkb, un.split + 1, splits) - kb_lo(nkb, un.split, splits);
       for (int i = 0; i < nk; ++i, ++it) {
         const int s = static_cast<int>(it % NST);
-        const uint32_t b = it & 1u;
-        if (!warp_wait_bounded(&sm.acc_empty[b], ((it >> 1) & 1u) ^ 1u, abort_flag, DEVERR_TIMEOUT_MMA) ||
+        const uint32_t b = it % M_BUFS;
+        if (!warp_wait_bounded(&sm.acc_empty[b], ((it / M_BUFS) & 1u) ^ 1u, abort_flag, DEVERR_TIMEOUT_MMA) ||
             !warp_wait_bounded(&sm.full[s], (it / NST) & 1u, abort_flag, DEVERR_TIMEOUT_MMA)) {
           ok = false;
           break;
@@ -721,10 +730,10 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       for (int j = 0; j < N / 2; ++j) acc[0][j] = acc[1][j] = make_float2(0.f, 0.f);
       for (int i = 0; i < nk; ++i, ++it) {
         const int q = static_cast<int>(it % Smem::kSaSlots);
-        const uint32_t b = it & 1u;
+        const uint32_t b = it % M_BUFS;
         if (!warp_wait_bounded(&sm.sa_full[q], (it / Smem::kSaSlots) & 1u, abort_flag,
                                DEVERR_TIMEOUT_EPILOGUE) ||
-            !warp_wait_bounded(&sm.acc_full[b], (it >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) {
+            !warp_wait_bounded(&sm.acc_full[b], (it / M_BUFS) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) {
           ok = false;
           break;
         }
@@ -861,7 +870,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 4 * N);
+    tmem_dealloc(tmem, 2 * M_BUFS * N);
   }
 }
 

@@ -17,6 +17,26 @@
 
 namespace w4a4 {
 
+// The codes of one block's 128 values, 8 per lane of a half-warp (every lane of
+// the warp takes part), and their scale.
+__device__ __forceinline__ float fp8_quant_half_warp(const uint4& v, uint2& codes) {
+  // magnitudes of bf16 pairs compare as 16-bit integers, infinities and NaN above all
+  uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                        __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const uint32_t eb = f8_scale_exp(max(m & 0xFFFFu, m >> 16) << 16);
+  codes = make_uint2(0u, 0u);
+  if (eb != 0u) {
+    const float inv = f8_inv_scale(eb);
+    codes.x = cvt_e4m3x4(bf16_lo_to_f32(v.x) * inv, bf16_hi_to_f32(v.x) * inv,
+                         bf16_lo_to_f32(v.y) * inv, bf16_hi_to_f32(v.y) * inv);
+    codes.y = cvt_e4m3x4(bf16_lo_to_f32(v.z) * inv, bf16_hi_to_f32(v.z) * inv,
+                         bf16_lo_to_f32(v.w) * inv, bf16_hi_to_f32(v.w) * inv);
+  }
+  return f8_scale(eb);
+}
+
 // One half-warp per (4 rows, one block): 16 lanes x 16 bytes cover a row's
 // 128 columns, the four rows' loads are independent, and the four scales of
 // consecutive tokens leave as one 16-byte store (scale is [blocks][ld_scale],
@@ -39,25 +59,9 @@ __device__ __forceinline__ void fp8_quant_rows4(const __nv_bfloat16* __restrict_
   float sc[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    // magnitudes of bf16 pairs compare as 16-bit integers, infinities and NaN above all
-    uint32_t m = __vmaxu2(__vmaxu2(v[r].x & 0x7FFF7FFFu, v[r].y & 0x7FFF7FFFu),
-                          __vmaxu2(v[r].z & 0x7FFF7FFFu, v[r].w & 0x7FFF7FFFu));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const uint32_t a = max(m & 0xFFFFu, m >> 16);
-    const uint32_t eb = f8_scale_exp(a << 16);
-    sc[r] = f8_scale(eb);
-    if (in && t0 + r < T) {
-      uint32_t c0 = 0u, c1 = 0u;
-      if (eb != 0u) {
-        const float inv = f8_inv_scale(eb);
-        c0 = cvt_e4m3x4(bf16_lo_to_f32(v[r].x) * inv, bf16_hi_to_f32(v[r].x) * inv,
-                        bf16_lo_to_f32(v[r].y) * inv, bf16_hi_to_f32(v[r].y) * inv);
-        c1 = cvt_e4m3x4(bf16_lo_to_f32(v[r].z) * inv, bf16_hi_to_f32(v[r].z) * inv,
-                        bf16_lo_to_f32(v[r].w) * inv, bf16_hi_to_f32(v[r].w) * inv);
-      }
-      *reinterpret_cast<uint2*>(q + (t0 + r) * d + col) = make_uint2(c0, c1);
-    }
+    uint2 c;
+    sc[r] = fp8_quant_half_warp(v[r], c);
+    if (in && t0 + r < T) *reinterpret_cast<uint2*>(q + (t0 + r) * d + col) = c;
   }
   if (hl == 0 && kb < nb)
     *reinterpret_cast<float4*>(scale + kb * ld_scale + t0) =
