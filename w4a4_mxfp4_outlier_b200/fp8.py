@@ -22,9 +22,16 @@ from dataclasses import dataclass, field
 
 import torch
 
-from . import (ERR_INVALID_ARG, W4A4Error, _check, _i64, _rows_bf16, _sig, _st, _vp)
+from . import (ERR_INVALID_ARG, OK, W4A4Error, _check, _i64, _rows_bf16, _sig, _st, _vp)
 
 BLOCK = 128
+_BF16, _F32 = torch.bfloat16, torch.float32
+
+# the handle of a device's current stream and the current device, without the
+# objects and checks around them where torch offers that (2 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class Fp8WeightC(ctypes.Structure):
@@ -46,14 +53,18 @@ def blocks(n: int) -> int:
 
 def _run(device: torch.device, stream, what: str, fn, *args):
     """fn(*args, stream) with `device` current; raises on a non-OK status."""
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, s), what)
+        s = _raw_stream(index)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == _device():
+        st = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, s), what)
+            st = fn(*args, s)
+    if st != OK:
+        _check(st, what)
 
 
 def _dense(t: torch.Tensor, dtypes, shape, device, what: str):
@@ -68,20 +79,33 @@ def _dense(t: torch.Tensor, dtypes, shape, device, what: str):
 
 def _bytes(t: torch.Tensor, device, what: str):
     """A workspace: any dense CUDA tensor on `device`."""
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
+    if t.device != device or not t.is_contiguous():
         raise W4A4Error(ERR_INVALID_ARG, f"{what}: the workspace must be a dense tensor on {device} "
                                          f"(got strides {tuple(t.stride())}, {t.device})")
 
 
-def _rows_out(Y: torch.Tensor, rows: int, cols: int, device, what: str) -> int:
-    """An output [rows, cols], bf16 or float32, unit column stride; its y_f32."""
-    if Y.dtype not in (torch.bfloat16, torch.float32) or tuple(Y.shape) != (rows, cols) or \
-            Y.device != device or (cols > 1 and Y.stride(1) != 1):
-        raise W4A4Error(ERR_INVALID_ARG,
-                        f"{what}: Y must be bfloat16 or float32 [{rows}, {cols}] on {device} with unit "
-                        f"column stride (got {Y.dtype}, {tuple(Y.shape)}, strides {tuple(Y.stride())}, "
-                        f"{Y.device})")
-    return int(Y.dtype == torch.float32)
+def _rows_in(X: torch.Tensor, cols: int, device, what: str):
+    """bf16 rows [T, cols] on `device`; T and the row stride."""
+    if X.dtype is _BF16 and X.is_cuda and X.device == device and X.dim() == 2:
+        (T, n), (ld, one) = X.shape, X.stride()
+        if n == cols and one == 1:
+            return T, ld if T > 1 else cols + 7 & ~7
+    _rows_bf16(X, what, device)
+    if X.shape[1] != cols:
+        raise W4A4Error(ERR_INVALID_ARG, f"{what}: X has {X.shape[1]} columns, not {cols}")
+    return X.shape[0], _ld(X)
+
+
+def _rows_out(Y: torch.Tensor, rows: int, cols: int, device, what: str):
+    """An output [rows, cols], bf16 or float32, unit column stride; its row stride and y_f32."""
+    f32 = Y.dtype is _F32
+    if (f32 or Y.dtype is _BF16) and Y.device == device and Y.shape == (rows, cols) and \
+            (cols <= 1 or Y.stride(1) == 1):
+        return _ld(Y), f32
+    raise W4A4Error(ERR_INVALID_ARG,
+                    f"{what}: Y must be bfloat16 or float32 [{rows}, {cols}] on {device} with unit "
+                    f"column stride (got {Y.dtype}, {tuple(Y.shape)}, strides {tuple(Y.stride())}, "
+                    f"{Y.device})")
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -99,6 +123,7 @@ class Fp8Weight:
     q: torch.Tensor
     scale: torch.Tensor
     c: Fp8WeightC = field(init=False, repr=False, compare=False)
+    device: torch.device = field(init=False, repr=False, compare=False)
 
     def __post_init__(self):
         if self.q.dim() not in (2, 3):
@@ -107,32 +132,30 @@ class Fp8Weight:
         _dense(self.q, _F8, self.q.shape, None, "Fp8Weight q")
         _dense(self.scale, (torch.float32,), lead + (blocks(d_out), blocks(d_in)), self.q.device,
                "Fp8Weight scale")
-        self.c = Fp8WeightC(d_in, d_out, lead[0] if lead else 1, self.q.data_ptr(),
-                            self.scale.data_ptr())
-
-    @property
-    def d_in(self) -> int:
-        return self.c.d_in
-
-    @property
-    def d_out(self) -> int:
-        return self.c.d_out
-
-    @property
-    def experts(self) -> int:
-        return self.c.experts
-
-    @property
-    def device(self) -> torch.device:
-        return self.q.device
+        self.device = self.q.device
+        self.d_in, self.d_out, self.experts = int(d_in), int(d_out), int(lead[0]) if lead else 1
+        self.c = Fp8WeightC(self.d_in, self.d_out, self.experts, self.q.data_ptr(), self.scale.data_ptr())
+        self._ref = ctypes.byref(self.c)
 
 
 @dataclass
 class Fp8Act:
     """Quantised activations: q uint8 [T, d], scale float32 [ceil(d/128), ld]
-    (token t and block b at [b, t]; ld is T rounded up to 4)."""
+    (token t and block b at [b, t]; ld is T rounded up to 4, or more)."""
     q: torch.Tensor
     scale: torch.Tensor
+
+    def __post_init__(self):
+        if self.q.dim() != 2 or self.scale.dim() != 2:
+            raise W4A4Error(ERR_INVALID_ARG, "Fp8Act: q and scale are 2-D")
+        self.T, self.d = (int(n) for n in self.q.shape)
+        self.ld, self.device = int(self.scale.shape[1]), self.q.device
+        if self.ld < (self.T + 3) // 4 * 4:
+            raise W4A4Error(ERR_INVALID_ARG, f"Fp8Act: no room for {self.T} scales in rows of {self.ld}")
+        if self.device.type == "cuda":
+            _dense(self.q, _F8, (self.T, self.d), self.device, "Fp8Act q")
+            _dense(self.scale, (_F32,), (blocks(self.d), self.ld), self.device, "Fp8Act scale")
+        self._args = self.q.data_ptr(), self.scale.data_ptr(), self.ld
 
 
 def alloc_act(T: int, d: int, device="cuda") -> Fp8Act:
@@ -141,13 +164,10 @@ def alloc_act(T: int, d: int, device="cuda") -> Fp8Act:
 
 
 def quant_act(X: torch.Tensor, out: Fp8Act, stream=None) -> Fp8Act:
-    T, d = X.shape if X.dim() == 2 else (-1, -1)
-    _rows_bf16(X, "fp8.quant_act")
-    _dense(out.q, _F8, (T, d), X.device, "fp8.quant_act q")
-    _dense(out.scale, (torch.float32,), (blocks(d), out.scale.shape[-1]), X.device,
-           "fp8.quant_act scale")
-    _run(X.device, stream, "fp8.quant_act", _quant_act, X.data_ptr(), T, d, _ld(X), out.q.data_ptr(),
-         out.scale.data_ptr(), out.scale.shape[1])
+    T, ld = _rows_in(X, out.d, out.device, "fp8.quant_act")
+    if T != out.T:
+        raise W4A4Error(ERR_INVALID_ARG, f"fp8.quant_act: X has {T} rows, out {out.T}")
+    _run(out.device, stream, "fp8.quant_act", _quant_act, X.data_ptr(), T, out.d, ld, *out._args)
     return out
 
 
@@ -163,19 +183,17 @@ def pack_weight(W: torch.Tensor, stream=None) -> Fp8Weight:
     w = Fp8Weight(torch.empty(W.shape, dtype=torch.uint8, device=W.device),
                   torch.empty(tuple(W.shape[:-2]) + (blocks(d_out), blocks(d_in)), dtype=torch.float32,
                               device=W.device))
-    _run(W.device, stream, "fp8.pack_weight", _pack_weight, W.data_ptr(), ldw, ctypes.byref(w.c))
+    _run(W.device, stream, "fp8.pack_weight", _pack_weight, W.data_ptr(), ldw, w._ref)
     return w
 
 
 def gemm(act: Fp8Act, w: Fp8Weight, Y: torch.Tensor, stream=None) -> torch.Tensor:
     """Y = act @ w^T, bf16 or float32 by Y's type."""
-    T = act.q.shape[0]
-    _dense(act.q, _F8, (T, w.d_in), w.device, "fp8.gemm q")
-    _dense(act.scale, (torch.float32,), (blocks(w.d_in), act.scale.shape[-1]), w.device,
-           "fp8.gemm scale")
-    f32 = _rows_out(Y, T, w.d_out, w.device, "fp8.gemm")
-    _run(w.device, stream, "fp8.gemm", _gemm, act.q.data_ptr(), act.scale.data_ptr(),
-         act.scale.shape[1], T, ctypes.byref(w.c), Y.data_ptr(), _ld(Y), f32)
+    if act.d != w.d_in or act.device != w.device:
+        raise W4A4Error(ERR_INVALID_ARG, f"fp8.gemm: activations of {act.d} columns on {act.device}, weight "
+                                         f"of {w.d_in} on {w.device}")
+    ld, f32 = _rows_out(Y, act.T, w.d_out, w.device, "fp8.gemm")
+    _run(w.device, stream, "fp8.gemm", _gemm, *act._args, act.T, w._ref, Y.data_ptr(), ld, f32)
     return Y
 
 
@@ -188,12 +206,10 @@ def workspace_size(T: int, w: Fp8Weight) -> int:
 def linear(X: torch.Tensor, w: Fp8Weight, workspace: torch.Tensor, Y: torch.Tensor,
            stream=None) -> torch.Tensor:
     """Y = quant_act(X) @ w^T, bf16 or float32 by Y's type."""
-    _rows_bf16(X, "fp8.linear", w.device)
-    T = X.shape[0]
-    if X.shape[1] != w.d_in:
-        raise W4A4Error(ERR_INVALID_ARG, f"fp8.linear: X has {X.shape[1]} columns, w {w.d_in}")
-    f32 = _rows_out(Y, T, w.d_out, w.device, "fp8.linear")
-    _bytes(workspace, w.device, "fp8.linear")
-    _run(w.device, stream, "fp8.linear", _linear, X.data_ptr(), T, _ld(X), ctypes.byref(w.c),
-         workspace.data_ptr(), workspace.numel() * workspace.element_size(), Y.data_ptr(), _ld(Y), f32)
+    dev = w.device
+    T, ldx = _rows_in(X, w.d_in, dev, "fp8.linear")
+    ldy, f32 = _rows_out(Y, T, w.d_out, dev, "fp8.linear")
+    _bytes(workspace, dev, "fp8.linear")
+    _run(dev, stream, "fp8.linear", _linear, X.data_ptr(), T, ldx, w._ref, workspace.data_ptr(),
+         workspace.nbytes, Y.data_ptr(), ldy, f32)
     return Y

@@ -19,8 +19,8 @@ from dataclasses import dataclass, field
 
 import torch
 
-from . import ERR_INVALID_ARG, W4A4Error, _check, _i64, _rows_bf16, _sig, _st, _vp
-from .fp8 import Fp8Weight, Fp8WeightC, _bytes, _dense, _ld, _rows_out, _run
+from . import ERR_INVALID_ARG, W4A4Error, _check, _i64, _sig, _st, _vp
+from .fp8 import Fp8Weight, Fp8WeightC, _bytes, _dense, _rows_in, _rows_out, _run
 
 GELU, SILU_GATED = 0, 1          # W4A4_MOE_GELU, W4A4_MOE_SILU_GATED
 MAX_TOKENS = 64
@@ -62,6 +62,7 @@ class MoE:
                                 f"{w.device}, not {up.experts} x {list(shape)} on {dev}")
         self.c = ExpertsC(self.top_k, self.act, int(self.renorm), self.router.data_ptr(),
                           self.gate.c if self.gate is not None else Fp8WeightC(), up.c, self.down.c)
+        self._ref = ctypes.byref(self.c)
 
 
 def workspace_size(T: int, m: MoE) -> int:
@@ -75,18 +76,15 @@ def forward(X: torch.Tensor, m: MoE, workspace: torch.Tensor, Y: torch.Tensor,
             stream=None) -> torch.Tensor:
     """Y = the layer of X, bf16 or float32 by Y's type; ids int32 and weights
     float32, both [T, top_k], receive the selection where given."""
-    up = m.up
-    _rows_bf16(X, "moe.forward", up.device)
-    T = X.shape[0]
-    if X.shape[1] != up.d_in:
-        raise W4A4Error(ERR_INVALID_ARG, f"moe.forward: X has {X.shape[1]} columns, the experts {up.d_in}")
-    f32 = _rows_out(Y, T, up.d_in, up.device, "moe.forward")
-    _bytes(workspace, up.device, "moe.forward")
+    d, dev = m.up.d_in, m.up.device
+    T, ldx = _rows_in(X, d, dev, "moe.forward")
+    ldy, f32 = _rows_out(Y, T, d, dev, "moe.forward")
+    _bytes(workspace, dev, "moe.forward")
     if ids is not None:
-        _dense(ids, (torch.int32,), (T, m.top_k), up.device, "moe.forward ids")
+        _dense(ids, (torch.int32,), (T, m.top_k), dev, "moe.forward ids")
     if weights is not None:
-        _dense(weights, (torch.float32,), (T, m.top_k), up.device, "moe.forward weights")
-    _run(up.device, stream, "moe.forward", _moe, X.data_ptr(), T, _ld(X), ctypes.byref(m.c),
-         workspace.data_ptr(), workspace.numel() * workspace.element_size(), Y.data_ptr(), _ld(Y), f32,
-         None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr())
+        _dense(weights, (torch.float32,), (T, m.top_k), dev, "moe.forward weights")
+    _run(dev, stream, "moe.forward", _moe, X.data_ptr(), T, ldx, m._ref, workspace.data_ptr(),
+         workspace.nbytes, Y.data_ptr(), ldy, f32, None if ids is None else ids.data_ptr(),
+         None if weights is None else weights.data_ptr())
     return Y
