@@ -49,6 +49,14 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
+// the two halves of cluster_sync_all
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   float s = bf16_lo_to_f32(a.x) * bf16_lo_to_f32(b.x);
   s = fmaf(bf16_hi_to_f32(a.x), bf16_hi_to_f32(b.x), s);
@@ -61,134 +69,140 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
-// One cluster per TG tokens.  A warp takes two experts at a time over a range
-// of the width (its lanes split it, 16 bytes each; the width is split where
-// there are fewer pairs of experts than warps); the sums of token i go to the
-// shared memory of the cluster's CTA i, whose first warp adds the ranges in
-// order and selects.
-template <int TG>
+template <int n>
+struct Steps {
+  static constexpr int value = n;
+};
+
+// One cluster per token (four tokens to a cluster read less and took longer: 16
+// tokens, 128 experts of 2048 columns, 13 against 6 us).  A warp takes two
+// experts at a time over a range of the width (its lanes split it, 16 bytes
+// each; the width is split where there are fewer pairs of experts than warps);
+// the sums go to the shared memory of the cluster's first CTA, which adds the
+// ranges in order and selects.
 __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_constant__ MoeArgs a) {
+  constexpr int U = 4;                 // steps of 256 columns whose loads are in flight together
   __shared__ float part[R_WARPS][kMoeMaxE];
   __shared__ float logits[kMoeMaxE];
+  __shared__ alignas(16) uint32_t key[kMoeMaxE];
+  __shared__ uint16_t chosen[kMoeMaxK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int t0 = static_cast<int>(blockIdx.x / R_CTAS) * TG;
-  const int nt = a.T - t0 < TG ? a.T - t0 : TG;
+  const int t = static_cast<int>(blockIdx.x / R_CTAS);
   const int epc = (a.E + R_CTAS - 1) / R_CTAS;               // experts per CTA
   const int pairs = (epc + 1) / 2;
   const int splits = pairs > 4 ? 1 : pairs > 2 ? 2 : pairs > 1 ? 4 : 8;
+  cluster_arrive();                    // (waited for before the first remote store)
   pdl_wait();
   pdl_launch_dependents();
-  cluster_sync_all();          // the other CTAs' shared memory exists
 
   if (warp >= R_WARPS) {
-    // counters of the next kernel, and x: one half-warp per block of 128 columns
+    // counters of the next kernel, and x, four tokens by every fourth cluster:
+    // one half-warp per block of 128 columns
     const int tid = threadIdx.x - 32 * R_WARPS;
     for (int i = blockIdx.x * 128 + tid; i < a.ncounters; i += gridDim.x * 128) a.counters[i] = 0;
     const int nb = (a.d + kFp8Block - 1) / kFp8Block;
     const int odd = (tid >> 4) & 1;
-    for (int kb = rank * 8 + (tid >> 4); kb - odd < nb; kb += R_CTAS * 8)
-      fp8_quant_rows4(a.X, a.T, a.d, a.ldx, a.xq, a.xs, a.ld_x, t0, kb);
+    if (t % 4 == 0)
+      for (int kb = rank * 8 + (tid >> 4); kb - odd < nb; kb += R_CTAS * 8)
+        fp8_quant_rows4(a.X, a.T, a.d, a.ldx, a.xq, a.xs, a.ld_x, t, kb);
+    cluster_wait();
   } else {
     const int e_end = (rank + 1) * epc < a.E ? (rank + 1) * epc : a.E;
     const int split = warp % splits;
-    const int steps = (a.d + 255) / 256;                     // 256 columns each
-    const int c_lo = 256 * (steps * split / splits), c_hi = 256 * (steps * (split + 1) / splits);
-    const int c_end = c_hi < a.d ? c_hi : a.d;
+    const int steps = (a.d + 255) / 256;
+    const int s_lo = steps * split / splits, s_hi = steps * (split + 1) / splits;
+    const int c_end = 256 * s_hi < a.d ? 256 * s_hi : a.d;
+    const __nv_bfloat16* xr = a.X + t * a.ldx;
+    bool waited = false;
     for (int e0 = rank * epc + 2 * (warp / splits); e0 < e_end; e0 += 2 * (R_WARPS / splits)) {
       const bool two = e0 + 1 < e_end;
       const __nv_bfloat16* r0 = a.router + static_cast<int64_t>(e0) * a.d;
       const __nv_bfloat16* r1 = two ? r0 + a.d : r0;
-      float acc[2][TG];
+      float acc0 = 0.f, acc1 = 0.f;
+      auto step = [&](int c0, auto count) {     // `count` steps: all their loads, then the sums
+        constexpr int n = decltype(count)::value;
+        uint4 w0[n], w1[n], x[n];
 #pragma unroll
-      for (int i = 0; i < TG; ++i) acc[0][i] = acc[1][i] = 0.f;
-#pragma unroll 4
-      for (int c = c_lo + 8 * lane; c < c_end; c += 256) {
-        const uint4 w0 = *reinterpret_cast<const uint4*>(r0 + c);
-        const uint4 w1 = *reinterpret_cast<const uint4*>(r1 + c);
-#pragma unroll
-        for (int i = 0; i < TG; ++i) {
-          const int t = i < nt ? t0 + i : t0;
-          const uint4 x = *reinterpret_cast<const uint4*>(a.X + t * a.ldx + c);
-          acc[0][i] += dot8(x, w0);
-          acc[1][i] += dot8(x, w1);
+        for (int u = 0; u < n; ++u) {
+          w0[u] = *reinterpret_cast<const uint4*>(r0 + c0 + 256 * u);
+          w1[u] = *reinterpret_cast<const uint4*>(r1 + c0 + 256 * u);
+          x[u] = *reinterpret_cast<const uint4*>(xr + c0 + 256 * u);
         }
+#pragma unroll
+        for (int u = 0; u < n; ++u) {
+          acc0 += dot8(x[u], w0[u]);
+          acc1 += dot8(x[u], w1[u]);
+        }
+      };
+      int c = 256 * s_lo + 8 * lane;
+      for (; c + 256 * (U - 1) < c_end; c += 256 * U) step(c, Steps<U>());
+      for (; c < c_end; c += 256) step(c, Steps<1>());
+      __syncwarp();
+      if (!waited) cluster_wait();
+      waited = true;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        acc0 += __shfl_xor_sync(0xFFFFFFFFu, acc0, o);
+        acc1 += __shfl_xor_sync(0xFFFFFFFFu, acc1, o);
       }
-#pragma unroll
-      for (int i = 0; i < TG; ++i) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          acc[0][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][i], o);
-          acc[1][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[1][i], o);
-        }
-        if (lane == 0 && i < nt) {
-          st_cluster_f32(mapa_shared(smem_u32(&part[split][e0]), i), acc[0][i]);
-          if (two) st_cluster_f32(mapa_shared(smem_u32(&part[split][e0 + 1]), i), acc[1][i]);
-        }
+      if (lane == 0) {
+        st_cluster_f32(mapa_shared(smem_u32(&part[split][e0]), 0), acc0);
+        if (two) st_cluster_f32(mapa_shared(smem_u32(&part[split][e0 + 1]), 0), acc1);
       }
+      __syncwarp();
     }
-  }
-  cluster_sync_all();
-  if (warp != 0 || rank >= nt) return;
-  for (int e = lane; e < a.E; e += 32) {
-    float l = part[0][e];
-    for (int s = 1; s < splits; ++s) l += part[s][e];
-    logits[e] = l;
+    if (!waited) cluster_wait();
   }
   __syncwarp();
+  cluster_sync_all();
+  if (rank != 0) return;
 
-  // Selection of token t0 + rank.  Keys order as the logits do; NaN comes last
-  // (key 1) and what has been taken is 0.
-  const int t = t0 + rank;
-  uint32_t key[kMoeMaxE / 32];
-  float lsum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMoeMaxE / 32; ++i) {
-    const int e = 32 * i + lane;
-    key[i] = 0u;
+  // Selection: every expert's place is the number of those before it.  Keys
+  // order as the logits do; NaN comes last.
+  const int e4 = (a.E + 3) & ~3;
+  for (int e = threadIdx.x; e < e4; e += R_THREADS) {
+    float l = 0.f;
+    uint32_t k = 0u;                   // (past the last expert: behind all)
     if (e < a.E) {
-      const float l = logits[e];
+      l = part[0][e];
+      for (int s = 1; s < splits; ++s) l += part[s][e];
       const uint32_t b = __float_as_uint(l);
-      key[i] = l != l ? 1u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+      k = l != l ? 1u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
     }
+    logits[e] = l;
+    key[e] = k;
   }
-  uint32_t mine_e = 0u;
-  float mine_l = 0.f, lmax = 0.f;
-  for (int j = 0; j < a.top_k; ++j) {
-    uint32_t best = 0u;
-    int bi = 0;
-#pragma unroll
-    for (int i = 0; i < kMoeMaxE / 32; ++i)
-      if (32 * i < a.E && key[i] > best) {   // the first of equal keys: the lower index
-        best = key[i];
-        bi = i;
-      }
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * bi + lane : 0xFFFFu);
-#pragma unroll
-    for (int i = 0; i < kMoeMaxE / 32; ++i)
-      if (e == 32u * i + lane) key[i] = 0u;
-    const float l = logits[e];
-    if (j == 0) lmax = l;
-    if (lane == j) {
-      mine_e = e;
-      mine_l = l;
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += R_THREADS) {
+    const uint32_t k = key[e];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < e4; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&key[j]);
+      before += (o.x > k || (o.x == k && j < e)) + (o.y > k || (o.y == k && j + 1 < e)) +
+                (o.z > k || (o.z == k && j + 2 < e)) + (o.w > k || (o.w == k && j + 3 < e));
     }
+    if (before < a.top_k) chosen[before] = static_cast<uint16_t>(e);
   }
-  const float ex = lane < a.top_k ? expf(mine_l - lmax) : 0.f;
-  if (a.renorm) {
-    lsum = ex;
-  } else {
-    for (int e = lane; e < a.E; e += 32) lsum += expf(logits[e] - lmax);
+  __syncthreads();
+  if (warp != 0) return;
+  const float lmax = logits[chosen[0]];
+  const int e = lane < a.top_k ? chosen[lane] : 0;
+  const float ex = lane < a.top_k ? expf(logits[e] - lmax) : 0.f;
+  float lsum = ex;
+  if (!a.renorm) {
+    lsum = 0.f;
+    for (int j = lane; j < a.E; j += 32) lsum += expf(logits[j] - lmax);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, o);
   if (lane < a.top_k) {
     const int at = t * a.top_k + lane;
     const float w = ex / lsum;
-    a.ids[at] = static_cast<int>(mine_e);
+    a.ids[at] = e;
     a.wts[at] = w;
-    if (a.ids_out) a.ids_out[at] = static_cast<int>(mine_e);
+    if (a.ids_out) a.ids_out[at] = e;
     if (a.wts_out) a.wts_out[at] = w;
   }
 }
@@ -211,11 +225,11 @@ __device__ __forceinline__ int moe_split(int units, int nkb, int most, int ctas,
   return 10 * static_cast<int>(best >> 5) < 9 * c1 ? static_cast<int>(best & 31u) + 1 : 1;
 }
 
-constexpr int M_THREADS = 384;     // weights, MMA, activations, idle, 4 epilogue, 4 finishing warps
+constexpr int M_THREADS = 512;     // weights, MMA, activations, idle, 8 epilogue, 4 finishing warps
 constexpr int M_W_BYTES = 2 * 128 * 128;
 constexpr int M_BUFS = 4;          // pairs of accumulators in tensor memory
 constexpr int M_UNITS = 4;         // units between the producer and the epilogue
-constexpr int M_CONSUMERS = 10;    // warps that read a unit: all but weights and idle
+constexpr int M_CONSUMERS = 14;    // warps that read a unit: all but weights and idle
 
 struct MoeUnit {
   int kind;          // 0: up, 1: down, 2: no more
@@ -451,13 +465,13 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     for (int s = 0; s < Smem::kSaSlots; ++s) mbar_init(&sm.sa_full[s], 1);
     for (int b = 0; b < M_BUFS; ++b) {
       mbar_init(&sm.acc_full[b], 1);
-      mbar_init(&sm.acc_empty[b], 4);
+      mbar_init(&sm.acc_empty[b], 8);
     }
     for (int u = 0; u < M_UNITS; ++u) {
       mbar_init(&sm.unit_full[u], 1);
       mbar_init(&sm.unit_empty[u], M_CONSUMERS);
     }
-    mbar_init(&sm.sums_full, 4);
+    mbar_init(&sm.sums_full, 8);
     mbar_init(&sm.sums_empty, 4);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0u;
@@ -705,12 +719,15 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     __syncwarp();
     mbar_wait_bounded(&sm.drain, 0u, nullptr, DEVERR_TIMEOUT_MMA);
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < 12) {
     // ============================ epilogue ================================
-    // Adds the K blocks' partial sums in registers and hands a unit's sums on.
+    // Four warps for each of the two tiles: add the K blocks' partial sums in
+    // registers and hand a unit's sums on.  (With four for both, 64 columns took
+    // them 1700 cycles a K block, more than its weights take to come.)
+    const int h = (warp - 4) >> 2;
     const int sp = warp & 3;
     const int tid = 32 * sp + lane;                    // the tile row of this thread
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16);
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16) + h * N;
     uint32_t it = 0;
     bool ok = true;
     for (uint32_t u = 0; ok; ++u) {
@@ -725,9 +742,9 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       const int nkb = un.kind == 0 ? nkb_d : nkb_f;
       const int splits = un.kind == 0 ? s_up : s_dn;
       const int nk = kb_lo(nkb, un.split + 1, splits) - kb_lo(nkb, un.split, splits);
-      float2 acc[2][N / 2];
+      float2 acc[N / 2];
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) acc[0][j] = acc[1][j] = make_float2(0.f, 0.f);
+      for (int j = 0; j < N / 2; ++j) acc[j] = make_float2(0.f, 0.f);
       for (int i = 0; i < nk; ++i, ++it) {
         const int q = static_cast<int>(it % Smem::kSaSlots);
         const uint32_t b = it % M_BUFS;
@@ -738,25 +755,24 @@ __global__ void __launch_bounds__(M_THREADS, 1)
           break;
         }
         tc_fence_after();
-        const float2 sb2 = sm.sb[q];
+        const float sb = h ? sm.sb[q].y : sm.sb[q].x;
+        const float2 sb2 = make_float2(sb, sb);
+        constexpr int CH = N < 32 ? 16 : 32;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float sb = h ? sb2.y : sb2.x;
+        for (int c = 0; c < N / CH; ++c) {
+          uint32_t r[CH];
+          if constexpr (CH == 16) tmem_ld_32x32b_x16(taddr + b * 2 * N + CH * c, r);
+          else tmem_ld_32x32b_x32(taddr + b * 2 * N + CH * c, r);
+          tmem_ld_wait_for(r);
 #pragma unroll
-          for (int c = 0; c < N / 16; ++c) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(taddr + b * 2 * N + h * N + 16 * c, r);
-            tmem_ld_wait_for(r);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][16 * c + 4 * j]);
-              float2& a0 = acc[h][8 * c + 2 * j];
-              float2& a1 = acc[h][8 * c + 2 * j + 1];
-              a0 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
-                              make_float2(s4.x * sb, s4.y * sb), a0);
-              a1 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
-                              make_float2(s4.z * sb, s4.w * sb), a1);
-            }
+          for (int j = 0; j < CH / 4; ++j) {
+            const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][CH * c + 4 * j]);
+            float2& a0 = acc[CH / 2 * c + 2 * j];
+            float2& a1 = acc[CH / 2 * c + 2 * j + 1];
+            a0 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
+                            __fmul2_rn(make_float2(s4.x, s4.y), sb2), a0);
+            a1 = __ffma2_rn(make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
+                            __fmul2_rn(make_float2(s4.z, s4.w), sb2), a1);
           }
         }
         tc_fence_before();
@@ -768,24 +784,23 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       // up: the columns are all tokens, those of this expert are kept; down: the
       // columns are the expert's pairs, then others'
       const uint64_t keep = un.kind == 0 ? mk : ~0ull >> (64 - __popcll(mk));
-      float* p = &sm.sums[0][tid];
+      float* p = &sm.sums[0][128 * h + tid];
 #pragma unroll
       for (int c = 0; c < N; ++c) {
         if ((keep >> c) & 1ull) {
-          p[0] = (c & 1) ? acc[0][c >> 1].y : acc[0][c >> 1].x;
-          p[128] = (c & 1) ? acc[1][c >> 1].y : acc[1][c >> 1].x;
+          *p = (c & 1) ? acc[c >> 1].y : acc[c >> 1].x;
           p += 256;
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.sums_full);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ============================ finishing ===============================
     // What follows a unit's sums, while the next unit's are made.  The four
     // warps agree at their barriers on whether one of them gave up
     // (named_bar_or), so none is left waiting for another.
-    const int tid = threadIdx.x - 256;
+    const int tid = threadIdx.x - 384;
     for (uint32_t u = 0;; ++u) {
       const int us = static_cast<int>(u % M_UNITS);
       bool ok = warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag,
@@ -974,8 +989,7 @@ cudaError_t plan_moe(const MoeArgs& a, int64_t E, const uint8_t* gate, const uin
 
 cudaError_t run_moe(const MoePlan& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  const int tg = p.a.T == 1 ? 1 : 4;
-  cfg.gridDim = dim3(static_cast<unsigned>(R_CTAS * ((p.a.T + tg - 1) / tg)));
+  cfg.gridDim = dim3(static_cast<unsigned>(R_CTAS * p.a.T));
   cfg.blockDim = dim3(R_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -985,7 +999,7 @@ cudaError_t run_moe(const MoePlan& p, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1 + static_cast<unsigned>(pdl_attrs(&attr[1]));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tg == 1 ? moe_route_kernel<1> : moe_route_kernel<4>, p.a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_route_kernel, p.a);
   if (e != cudaSuccess) return e;
   if (p.gated)
     return p.n == 16 ? run_moe_experts<16, true>(p, stream)
