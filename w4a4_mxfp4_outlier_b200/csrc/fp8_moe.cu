@@ -12,7 +12,8 @@
 //  * moe_route_kernel: router logits, selection, quantisation of x.
 //  * moe_experts_kernel: persistent.  All CTAs take work units from one counter:
 //    first the units of the up projections, then those of the down
-//    projections; a unit is two tiles of 128 weight rows over a range of K.
+//    projections, in an order that lets the first down units find the blocks of
+//    h they need complete; a unit is two tiles of 128 weight rows over a range of K.
 //    Each unit's float32 sums go to the workspace (a few columns: little beside
 //    the weights) and the last unit of a block to arrive finishes it in a fixed
 //    order, so results do not depend on timing: for an up block the activation
@@ -20,7 +21,8 @@
 //    experts.  The weight tiles of the following units, those of down units
 //    included, are fetched while h is still being made, so the memory pipe does
 //    not drain between the two projections.
-//    A unit of the down projection waits until its expert's h is complete.
+//    A unit of the down projection waits until its range of its expert's h is
+//    complete.
 //    All up units were taken, by running CTAs that wait for nothing, before the
 //    first down unit is: the wait ends however few CTAs of the grid run at once.
 #include <cuda.h>
@@ -34,9 +36,6 @@ constexpr int kMoeMaxT = 64;
 constexpr int kMoeMaxE = 512;
 constexpr int kMoeMaxK = 16;
 constexpr int kMoeMaxSplit = 8;
-#ifndef MOE_JOIN
-#define MOE_JOIN 8
-#endif
 
 // ---------------------------------------------------------------------------
 // Router
@@ -524,8 +523,9 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       n += __popc(any);
       rows += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
-    const int su = moe_split(n * up_units, nkb_d, a.most_up, static_cast<int>(gridDim.x), MOE_JOIN);
-    const int sd = moe_split(n * dn_tiles, nkb_f, a.most_dn, static_cast<int>(gridDim.x), 0);
+    const int ctas = static_cast<int>(gridDim.x);
+    const int su = moe_split(n * up_units, nkb_d, a.most_up, ctas, 8);
+    const int sd = moe_split(n * dn_tiles, nkb_f, a.most_dn, ctas, 0);
     if (lane == 0) {
       sm.n_act = n;
       sm.s_up = su;
@@ -557,15 +557,17 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       MoeUnit un;
       if (cur < n_up) {
         un.kind = 0;
-        un.split = cur % s_up;
-        un.blk = (cur / s_up) % up_units;
-        un.ex = cur / (s_up * up_units);
+        const int c = cur / s_up;
+        un.split = cur - c * s_up;
+        un.ex = s_dn > 1 ? c % n_act : c / up_units;
+        un.blk = s_dn > 1 ? c / n_act : c % up_units;
       } else if (cur < n_all) {
         const int v = cur - n_up;
         un.kind = 1;
-        un.split = v % s_dn;
-        un.ex = (v / s_dn) % n_act;
-        un.blk = v / (s_dn * n_act);
+        const int c = v / dn_tiles;
+        un.blk = v - c * dn_tiles;
+        un.split = c / n_act;
+        un.ex = c - un.split * n_act;
       } else {
         un.kind = 2;
         un.split = un.ex = un.blk = 0;
@@ -644,8 +646,9 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       const int k0 = kb_lo(nkb, un.split, splits), k1 = kb_lo(nkb, un.split + 1, splits);
       WarpRun r0(sb0 + k0, k1 - k0), r1(sb1 + k0, k1 - k0);
       if (un.kind == 1) {
-        const bool got = counter_wait_bounded(a.ready + un.ex, up_units, abort_flag,
-                                              DEVERR_TIMEOUT_PRODUCER);
+        bool got = true;
+        for (int kb = k0 + lane; kb < k1 && got; kb += 32)
+          got = counter_wait_bounded(a.ready + un.ex * nkb_f + kb, 1, abort_flag, DEVERR_TIMEOUT_PRODUCER);
         if (!__all_sync(0xFFFFFFFFu, got)) break;
         fence_proxy_async_global();
       }
@@ -851,7 +854,9 @@ __global__ void __launch_bounds__(M_THREADS, 1)
           named_bar_sync(1, 128);
           if (tid == 0) {
             __threadfence();
-            atomicAdd(a.ready + un.ex, 1);
+            int* flag = a.ready + un.ex * nkb_f + (kGated ? un.blk : 2 * un.blk);
+            atomicExch(flag, 1);
+            if (!kGated && 2 * un.blk + 1 < nkb_f) atomicExch(flag + 1, 1);
           }
         }
       } else {
@@ -925,7 +930,7 @@ MoeLayout moe_layout(int64_t T, int64_t d, int64_t ff, int64_t E, int64_t top_k,
   const int64_t nE = E < P ? E : P;
   l.up_done = 0;
   l.ready = l.up_done + nE * up_units;
-  l.dn_done = l.ready + nE;
+  l.dn_done = l.ready + nE * nkb_f;
   l.ticket = l.dn_done + 1;
   l.ncounters = l.ticket + 1;
   size_t at = 0;
