@@ -127,7 +127,9 @@ def _to_gpu(aq, sa, wq, sw):
 SHAPES = [(1, 16, 16), (1, 2048, 144), (2, 128, 128), (15, 400, 272), (16, 1040, 128), (17, 256, 16),
           (32, 5120, 256), (33, 144, 528), (64, 1168, 384), (65, 2048, 272), (127, 272, 1040),
           (128, 512, 128), (129, 640, 400), (257, 1040, 272), (512, 256, 528), (513, 272, 272),
-          (600, 2064, 1552), (769, 128, 16), (1100, 1296, 784)]
+          (600, 2064, 1552), (769, 128, 16), (1100, 1296, 784),
+          # more tiles than CTA pairs, an odd number of K blocks: buffers and stages change places
+          (2600, 400, 2064)]
 
 
 @pytest.mark.parametrize("T,d_in,d_out", SHAPES)

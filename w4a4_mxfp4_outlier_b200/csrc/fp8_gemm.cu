@@ -192,9 +192,7 @@ __global__ void __launch_bounds__(F_THREADS, 2)
 #pragma unroll
       for (int c = 0; c < N / CH; ++c) {
         uint32_t r[CH];
-        if constexpr (CH == 16) tmem_ld_32x32b_x16(taddr + b * N + c * CH, r);
-        else tmem_ld_32x32b_x32(taddr + b * N + c * CH, r);
-        tmem_ld_wait_for(r);
+        tmem_ld_now(taddr + b * N + c * CH, r);
 #pragma unroll
         for (int j = 0; j < CH / 4; ++j) {
           const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][c * CH + 4 * j]);
@@ -471,26 +469,20 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      // What bounds the kernel: the tensor cores need 560 cycles per K block
-      // (measured without this loop: 190 us at T = 4096, 5120 -> 13824), this
-      // loop about 850 (260 us), of which the additions themselves take 330
-      // (100 FMAs per cycle and SM).  Measured and no faster: 16 warps of 64
-      // columns (268 us), MMAs of 128 columns with a buffer pair per half (267),
-      // one 32-column load at a time (276), scalar FMAs (283), the next block's
-      // loads before the last additions (299).  A wait that fails (it ends in
+      // What bounds the kernel: the chain through a buffer.  Its MMAs run 512
+      // cycles (560 a K block measured without this loop: 190 us at T = 4096,
+      // 5120 -> 13824), then commit, this warp's look (120), loads and arrival
+      // (250), the issuer's look (165) and its issuing (200) follow one another;
+      // with two buffers that makes about 850 cycles a K block (260 us).  The
+      // additions themselves take 330 (100 FMAs per cycle and SM).  Measured and
+      // no faster: 16 warps of 64 columns (268 us), MMAs of 128 columns with a
+      // buffer pair per half (267), 32-column loads (262 to 276), scalar FMAs
+      // (283), the next block's loads before the last additions (299), the
+      // issuer's looks ahead of its MMAs (276).  A wait that fails (it ends in
       // bounded time, and all later ones then fail at once) only clears `ok`,
       // which is looked at once per tile.
       bool ok = true;
       float m = 0.f;
-      uint32_t r[2][32];
-      auto add = [&](int c, float w) {
-        const float2 m2 = make_float2(w, w);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          acc[16 * c + j] = __ffma2_rn(make_float2(__uint_as_float(r[c & 1][2 * j]),
-                                                   __uint_as_float(r[c & 1][2 * j + 1])),
-                                       m2, acc[16 * c + j]);
-      };
       // scale of K block kb, and its sums complete
       auto next_block = [&](int kb, uint32_t gk) {
         const uint32_t q = grp & 1u;
@@ -511,21 +503,21 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         const uint32_t b = g & 1u;
         const uint32_t ta = taddr + 256u * b;
         next_block(kb, g);
-        tmem_ld_32x32b_x32(ta, r[0]);
-        tmem_ld_32x32b_x32(ta + 32, r[1]);
-        tmem_ld_wait_for(r[0]);
-        tmem_ld_waited(r[1]);
-        add(0, m);
-        tmem_ld_32x32b_x32(ta + 64, r[0]);
-        add(1, m);
-        tmem_ld_32x32b_x32(ta + 96, r[1]);
-        tmem_ld_wait_for(r[0]);
-        tmem_ld_waited(r[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(acc_empty_leader + 8u * b);
-        add(2, m);
-        add(3, m);
+        const float2 m2 = make_float2(m, m);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[64];
+          tmem_ld_now(ta + 64 * c, r);
+          if (c == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(acc_empty_leader + 8u * b);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            acc[32 * c + j] = __ffma2_rn(
+                make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), m2, acc[32 * c + j]);
+        }
       }
       if (__any_sync(0xFFFFFFFFu, !ok)) break;
       // Y through staging blocks of 16 rows x 64 bytes (64-byte swizzle), as

@@ -10,21 +10,35 @@
 //
 // With few tokens the layer is the reading of the chosen experts' weights.
 //  * moe_route_kernel: router logits, selection, quantisation of x.
-//  * moe_experts_kernel: persistent.  All CTAs take work units from one counter:
-//    first the units of the up projections, then those of the down
-//    projections, in an order that lets the first down units find the blocks of
-//    h they need complete; a unit is two tiles of 128 weight rows over a range of K.
-//    Each unit's float32 sums go to the workspace (a few columns: little beside
-//    the weights) and the last unit of a block to arrive finishes it in a fixed
-//    order, so results do not depend on timing: for an up block the activation
-//    and the e4m3 codes of h, for 256 columns of y the weighted sum over
-//    experts.  The weight tiles of the following units, those of down units
-//    included, are fetched while h is still being made, so the memory pipe does
-//    not drain between the two projections.
+//  * moe_experts_kernel: persistent, one CTA per SM.  All CTAs take work units
+//    from one counter: first the units of the up projections, then those of the
+//    down projections, in an order that lets the first down units find the
+//    blocks of h they need complete; a unit is two tiles of 128 weight rows over
+//    a range of K.  The roles of a CTA run ahead of each other: weight tiles of
+//    the following units, down units included, are fetched while h is still
+//    being made, and a finishing warp group takes a unit's sums from shared
+//    memory (a few columns: little beside the weights) while the next unit's are
+//    made: for an up unit the activation and the e4m3 codes of h, for a down
+//    unit float32 sums to the workspace.  Where K of an up unit is split (few
+//    units), the last range to arrive adds the ranges in their order; y is summed
+//    at the end by all CTAs, in the order of selection: results do not depend on
+//    timing.
 //    A unit of the down projection waits until its range of its expert's h is
-//    complete.
-//    All up units were taken, by running CTAs that wait for nothing, before the
-//    first down unit is: the wait ends however few CTAs of the grid run at once.
+//    complete.  All up units were taken, by running CTAs that wait for nothing,
+//    before the first down unit is: the wait ends however few CTAs of the grid
+//    run at once.
+//
+// Measured (back to back, three sets of weights in turn): 64 tokens, 64 experts
+// of 5120 x 1536, 8 chosen: 272 us, 5.55 TB/s of the weights met; 16 tokens, 128
+// experts of 2048 x 768, 8 chosen: 71 us, 5.5 TB/s; 1 token, 2 of 8 experts of
+// 5120 x 13824: 79 us, 5.4 TB/s; 1 token, 6 of 64 experts of 2048 x 1024: 26 us,
+// of which the router takes 5.5 and the chain route -> up -> down -> y the rest
+// (about ten round trips to memory one after the other).
+// What brought it there: the finishing warps beside the epilogue (64 tokens 787
+// -> 305 us; before, the memory idled while a unit was finished, and the sums of
+// y were made by whichever CTA ended a tile's units, mostly the same one); eight
+// epilogue warps (300 -> 274); order of the units and flags per block of h (1
+// token, 2 of 8 experts: 84 -> 79).
 #include <cuda.h>
 
 #include "fp8_device.cuh"
@@ -764,9 +778,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
 #pragma unroll
         for (int c = 0; c < N / CH; ++c) {
           uint32_t r[CH];
-          if constexpr (CH == 16) tmem_ld_32x32b_x16(taddr + b * 2 * N + CH * c, r);
-          else tmem_ld_32x32b_x32(taddr + b * 2 * N + CH * c, r);
-          tmem_ld_wait_for(r);
+          tmem_ld_now(taddr + b * 2 * N + CH * c, r);
 #pragma unroll
           for (int j = 0; j < CH / 4; ++j) {
             const float4 s4 = *reinterpret_cast<const float4*>(&sm.sa[q][CH * c + 4 * j]);
