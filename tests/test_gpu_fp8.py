@@ -129,7 +129,10 @@ SHAPES = [(1, 16, 16), (1, 2048, 144), (2, 128, 128), (15, 400, 272), (16, 1040,
           (128, 512, 128), (129, 640, 400), (257, 1040, 272), (512, 256, 528), (513, 272, 272),
           (600, 2064, 1552), (769, 128, 16), (1100, 1296, 784),
           # more tiles than CTA pairs, an odd number of K blocks: buffers and stages change places
-          (2600, 400, 2064)]
+          (2600, 400, 2064),
+          # K split over clusters of 5, 5, 5, 5, 4, 3 and 2, in even and uneven ranges
+          (66, 1808, 16), (65, 3856, 400), (128, 5120, 256), (129, 4000, 2576), (100, 4112, 7184),
+          (200, 4752, 4624), (260, 6416, 4880)]
 
 
 @pytest.mark.parametrize("T,d_in,d_out", SHAPES)
@@ -268,6 +271,35 @@ def test_two_streams():
     torch.cuda.synchronize()
     for _, _, Y, Z, _ in jobs:
         assert torch.equal(Y, Z)
+    _no_error()
+
+
+def test_split_k_captured_beside_another_stream():
+    # clusters that join through shared memory, in a graph and eagerly at once;
+    # a token that is not finite touches no other
+    rng = _rng(15)
+    w = fp8.pack_weight(_bf16(0.02 * rng.standard_normal((1040, 4112))))
+    T = 150
+    X, V = _acts(rng, T, 4112), _acts(rng, T, 4112)
+    ws, ws2 = (torch.empty(fp8.workspace_size(T, w), dtype=torch.uint8, device="cuda") for _ in range(2))
+    Y, Z, U, R, S = (torch.empty(T, 1040, dtype=torch.bfloat16, device="cuda") for _ in range(5))
+    fp8.linear(X, w, ws, R)
+    fp8.linear(V, w, ws, S)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fp8.linear(X, w, ws, Y)
+        fp8.linear(X, w, ws, Z)
+    other = torch.cuda.Stream()
+    for _ in range(5):
+        g.replay()
+        fp8.linear(V, w, ws2, U, stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, R) and torch.equal(Z, R) and torch.equal(U, S)
+    X[149, 4100] = float("inf")
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.isnan(Y[149]).all() and torch.equal(Y[:149], R[:149])
     _no_error()
 
 

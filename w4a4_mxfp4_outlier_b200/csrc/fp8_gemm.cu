@@ -10,9 +10,12 @@
 // accumulator buffers in tensor memory let the tensor cores work on the next K
 // block meanwhile.
 //
-// Two kernels:
+// Three kernels:
 //  * fp8_gemm_pair_kernel: CTA pairs (cta_group::2), 256 tokens x 256 channels
 //    per tile, persistent.
+//  * fp8_gemm_mid_kernel: for products whose tiles of 256 x 256 would leave most
+//    SMs idle: 128 tokens x 256 channels per CTA, and the CTAs of a cluster split K
+//    and join their sums in the same way.
 //  * fp8_gemm_few_kernel: for few tokens, where reading the weight is the
 //    work: the weight rows are the MMA's M (128 per CTA), the tokens its N
 //    (16 .. 64), and the CTAs of a cluster split K and join their sums through
@@ -257,6 +260,276 @@ __global__ void __launch_bounds__(F_THREADS, 2)
   cluster_sync_all();          // no CTA leaves while another reads its sums
 }
 
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// ---------------------------------------------------------------------------
+// K split over a cluster
+// ---------------------------------------------------------------------------
+constexpr int H_STAGES = 4;
+constexpr int H_X_BYTES = 128 * 128;                  // 128 token rows
+constexpr int H_STAGE_BYTES = 3 * H_X_BYTES;          // and 256 weight rows
+constexpr int H_THREADS = 384;                        // producer, MMA, 2 idle, 8 epilogue warps
+constexpr int H_EPI_WARPS = 8;
+constexpr int H_GROUP_M = 16;
+constexpr int H_SA_GROUP = 8;
+constexpr int H_MAX_C = 5;                            // CTAs of a cluster
+
+struct MidSmem {
+  uint8_t stage[H_STAGES][H_STAGE_BYTES];
+  // scales of the 128 tokens, for groups of 8 K blocks in turn
+  alignas(16) float sa[2][H_SA_GROUP][128];
+  uint64_t sa_full[2];
+  uint64_t sa_empty[2];
+  uint64_t full[H_STAGES];
+  uint64_t empty[H_STAGES];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+  static_assert(128 * 256 * 4 <= H_STAGES * H_STAGE_BYTES, "the sums fit the ring");
+};
+
+__global__ void __launch_bounds__(H_THREADS, 1)
+    fp8_gemm_mid_kernel(const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_w,
+                        const __grid_constant__ Fp8GemmArgs args) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  MidSmem& sm = *reinterpret_cast<MidSmem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  volatile uint32_t* abort_flag = &sm.abort_flag;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int C = static_cast<int>(gridDim.z);              // cluster = CTAs along z, one K range each
+  const int rank = static_cast<int>(blockIdx.z);
+  int tm, tn;
+  tile_coords<H_GROUP_M>(blockIdx.x, args.tiles_m, args.tiles_n, tm, tn);
+  const int m0 = tm * 128, n0 = tn * 256;
+  const int rows = args.T - m0 < 128 ? args.T - m0 : 128;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(args.nkb) * rank / C);
+  const int nk = static_cast<int>(static_cast<int64_t>(args.nkb) * (rank + 1) / C) - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < H_STAGES; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.sa_full[s], 1);
+      mbar_init(&sm.sa_empty[s], H_EPI_WARPS);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], H_EPI_WARPS);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0u;
+    fence_barrier_init();
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp < 4) {
+    // the launch's 384 x 168 registers: 128 x 56 here, 256 x 224 for the epilogue
+    setmaxnreg_dec<56>();
+    if (warp == 0) {
+      // ============================ TMA producer ==========================
+      uint32_t issued = 0, s = 0, ph = 0;
+      const uint32_t sa_bytes = static_cast<uint32_t>((rows + 3) & ~3) * 4u;
+      for (int i = 0; i < nk; ++i) {
+        if (i % H_SA_GROUP == 0) {
+          const uint32_t grp = i / H_SA_GROUP, q = grp & 1u;
+          if (grp >= 2 && !warp_wait_bounded(&sm.sa_empty[q], ((grp >> 1) & 1u) ^ 1u, abort_flag,
+                                             DEVERR_TIMEOUT_PRODUCER))
+            break;
+          if (elect_one()) {
+            const int n = nk - i < H_SA_GROUP ? nk - i : H_SA_GROUP;
+            mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes * n);
+            for (int j = 0; j < n; ++j)
+              bulk_load(sm.sa[q][j], args.sa + (kb0 + i + j) * args.ld_sa + m0, sa_bytes, &sm.sa_full[q]);
+          }
+          __syncwarp();
+          issued = 1;
+        }
+        if (i >= H_STAGES && !warp_wait_bounded(&sm.empty[s], ph ^ 1u, abort_flag, DEVERR_TIMEOUT_PRODUCER))
+          break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.full[s], H_STAGE_BYTES);
+          tma_load_2d(sm.stage[s], &tm_x, &sm.full[s], (kb0 + i) * 128, m0);
+          tma_load_2d(sm.stage[s] + H_X_BYTES, &tm_w, &sm.full[s], (kb0 + i) * 128, n0);
+        }
+        __syncwarp();
+        if (++s == H_STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (issued != 0 && *abort_flag) spin_ns(200000);   // copies in flight land before teardown
+      __syncwarp();
+    } else if (warp == 1) {
+      // ============================ MMA issuer ============================
+      constexpr uint32_t ID = idesc_f8(128, 256);
+      const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]));
+      const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(sm.stage[0]) + H_X_BYTES);
+      uint32_t s = 0, ph = 0;
+      uint64_t soff = 0;
+      for (int i = 0; i < nk; ++i) {
+        const uint32_t b = i & 1;
+        if (!warp_wait_bounded(&sm.full[s], ph, abort_flag, DEVERR_TIMEOUT_MMA) ||
+            !warp_wait_bounded(&sm.acc_empty[b], ((i >> 1) & 1u) ^ 1u, abort_flag, DEVERR_TIMEOUT_MMA))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + 256u * b;
+          mma_f8(d, da0 + soff + 0, db0 + soff + 0, ID, 0u);
+          mma_f8(d, da0 + soff + 2, db0 + soff + 2, ID, 1u);
+          mma_f8(d, da0 + soff + 4, db0 + soff + 4, ID, 1u);
+          mma_f8(d, da0 + soff + 6, db0 + soff + 6, ID, 1u);
+          tc_commit(&sm.acc_full[b]);
+          tc_commit(&sm.empty[s]);
+        }
+        __syncwarp();
+        soff += H_STAGE_BYTES >> 4;
+        if (++s == H_STAGES) {
+          s = 0;
+          ph ^= 1u;
+          soff = 0;
+        }
+      }
+      if (elect_one()) tc_commit(&sm.drain);
+      __syncwarp();
+      mbar_wait_bounded(&sm.drain, 0u, nullptr, DEVERR_TIMEOUT_MMA);
+      __syncwarp();
+    }
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    // ============================ epilogue ================================
+    // Each warp owns 32 rows (its lanes) x 128 columns: 128 sums a lane.
+    setmaxnreg_inc<224>();
+    const int ew = warp - 4;
+    const int sp = warp & 3;
+    const int half = ew >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * sp) << 16) + 128 * half;
+    const int nblk = tn * 2 + half;
+    // (a block past d_out reads nothing; rows past T have any scale, and are not stored)
+    WarpRun sbr(args.sb + static_cast<int64_t>(nblk) * args.nkb + kb0, nblk * 128 < args.d_out ? nk : 0);
+    float2 acc[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+    // A wait that fails (it ends in bounded time, and all later ones then fail
+    // at once) also raises abort_flag, which is looked at behind the loop.
+    for (int i = 0; i < nk; ++i) {
+      const uint32_t grp = i / H_SA_GROUP, q = grp & 1u, b = i & 1;
+      const int qi = i % H_SA_GROUP;
+      if (qi == 0)
+        mbar_wait_bounded(&sm.sa_full[q], (grp >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+      const float m = sm.sa[q][qi][32 * sp + lane] * sbr.get(i);
+      mbar_wait_bounded(&sm.acc_full[b], (i >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+      __syncwarp();
+      tc_fence_after();
+      if (qi == H_SA_GROUP - 1 && lane == 0) mbar_arrive(&sm.sa_empty[q]);   // (all lanes have read theirs)
+      const float2 m2 = make_float2(m, m);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[64];
+        tmem_ld_now(taddr + 256u * b + 64 * c, r);
+        if (c == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          acc[32 * c + j] = __ffma2_rn(
+              make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), m2, acc[32 * c + j]);
+      }
+    }
+    __syncwarp();
+    // This CTA's sums over its own ring (its last accumulator is complete, so
+    // every tile has arrived and been read): [8 columns][half of them][row][4].
+    // Each rank then joins its share of the tile.  Pulling the others' sums costs
+    // less than their pushing them did (128 tokens, 5120 -> 5120: 15.1 us, 16.4).
+    const uint32_t ring = smem_u32(sm.stage[0]);
+    const int row = 32 * sp + lane;
+    if (*abort_flag == 0u && row < rows) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int u = 16 * half + v;
+        const uint32_t at = ring + 4096u * u + 16u * row;
+        st_shared_f32x4(at, acc[4 * v], acc[4 * v + 1]);
+        st_shared_f32x4(at + 2048u, acc[4 * v + 2], acc[4 * v + 3]);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    if (*abort_flag == 0u) {
+      // pieces of 8 rows (8 lanes) x 8 columns, the ranks' sums in order
+      const int pieces = 32 * ((rows + 7) >> 3);
+      const int end = pieces * (rank + 1) / C;
+      for (int i = pieces * rank / C + 4 * ew + (lane >> 3); i < end; i += 4 * H_EPI_WARPS) {
+        const int r = 8 * (i >> 5) + (lane & 7), col = n0 + 8 * (i & 31);
+        if (r >= rows || col >= args.d_out) continue;      // d_out is a multiple of 16
+        const uint32_t at = ring + 4096u * (i & 31) + 16u * r;
+        float4 v[H_MAX_C][2];
+#pragma unroll
+        for (int k = 0; k < H_MAX_C; ++k)
+          if (k < C) {
+            const uint32_t from = mapa_shared(at, k);
+            v[k][0] = ld_cluster_f32x4(from);
+            v[k][1] = ld_cluster_f32x4(from + 2048u);
+          }
+        float4 x = v[0][0], y = v[0][1];
+#pragma unroll
+        for (int k = 1; k < H_MAX_C; ++k)
+          if (k < C) {
+            const float4 a = v[k][0], b = v[k][1];
+            x.x += a.x; x.y += a.y; x.z += a.z; x.w += a.w;
+            y.x += b.x; y.y += b.y; y.z += b.z; y.w += b.w;
+          }
+        const int64_t out = static_cast<int64_t>(m0 + r) * args.ldy + col;
+        if (args.y_f32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(args.Y) + out);
+          o[0] = x;
+          o[1] = y;
+        } else {
+          const __nv_bfloat162 p[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                                       __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.Y) + out) =
+              *reinterpret_cast<const uint4*>(p);
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  cluster_sync_all();          // no CTA leaves while another reads its sums
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // CTA pairs
 // ---------------------------------------------------------------------------
@@ -283,15 +556,6 @@ struct Fp8PairSmem {
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
-
-template <int kRegs>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 
 template <bool kF32>
 __global__ void __launch_bounds__(Q_THREADS, 1)
@@ -594,6 +858,18 @@ static cudaError_t few_attr() {
   return e;
 }
 
+static cudaError_t mid_attr() {
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(fp8_gemm_mid_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(MidSmem) + 1024));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
+  return e;
+}
+
 static int fp8_pair_capacity() {
   static int cached[64] = {0};
   int dev = 0;
@@ -665,6 +941,33 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
       return cudaErrorInvalidValue;
     return cudaSuccess;
   }
+  a.tiles_m = static_cast<int>((T + 127) / 128);
+  a.tiles_n = static_cast<int>((d_out + 255) / 256);
+  // Where the tiles leave SMs idle, K is split over the CTAs of a cluster.  The
+  // join costs 2 us (two CTAs, few rows) to 6 us (five, 128 rows), a K block
+  // 0.43 us in either kernel, so the split has to spare some.  120 CTAs in
+  // clusters of up to 5 run at once, 140 in clusters of 7 were seen not to.
+  // linear(), us, pair kernel and this one (CTAs of a cluster): 128 x 5120 x 5120
+  // 23.3, 15.1 (5); 256 x 5120 x 5120 24.4, 19.8 (3); 300 x 5120 x 5120 25.0, 25.0
+  // (2); 128 x 13824 x 5120 52.1, 25.0 (5); 384 x 13824 x 5120 57.8, 40.5 (2);
+  // 128 x 2048 x 5120 13.1, 12.2 (5); 128 x 1024 x 1024, which spares 6 blocks,
+  // 9.6, 10.4.
+  const int64_t mid_tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+  int C = 1;
+  for (int c = 2; c <= H_MAX_C; ++c)
+    if (mid_tiles * c <= 120) C = c;
+  if (a.nkb - (a.nkb + C - 1) / C >= 12) {
+    const cudaError_t e = mid_attr();
+    if (e != cudaSuccess) return e;
+    p->mid = true;
+    p->cluster = C;
+    p->grid = dim3(static_cast<unsigned>(mid_tiles), 1, C);
+    p->smem = sizeof(MidSmem) + 1024;
+    if (!make_tmap(&p->tm_x, aq, u8, 1, d_in, T, d_in, 128) ||
+        !make_tmap(&p->tm_w, wq, u8, 1, d_in, d_out, d_in, 256))
+      return cudaErrorInvalidValue;
+    return cudaSuccess;
+  }
   const int cap = fp8_pair_capacity();
   if (cap <= 0) return cudaErrorInvalidConfiguration;
   a.tiles_m = static_cast<int>((T + 255) / 256);
@@ -702,6 +1005,11 @@ cudaError_t run_fp8_gemm(const Fp8GemmPlan& p, cudaStream_t stream) {
     void (*k)(CUtensorMap, CUtensorMap, Fp8GemmArgs) =
         p.few == 16 ? fp8_gemm_few_kernel<16> : p.few == 32 ? fp8_gemm_few_kernel<32> : fp8_gemm_few_kernel<64>;
     return cudaLaunchKernelEx(&cfg, k, p.tm_w, p.tm_x, p.a);
+  }
+  if (p.mid) {
+    cfg.blockDim = dim3(H_THREADS, 1, 1);
+    attr[0].val.clusterDim.z = static_cast<unsigned>(p.cluster);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_mid_kernel, p.tm_x, p.tm_w, p.a);
   }
   cfg.blockDim = dim3(Q_THREADS, 1, 1);
   attr[0].val.clusterDim.x = 2;

@@ -16,7 +16,7 @@ struct Fp8GemmArgs {
   void* Y;
   int64_t ld_sa, ldy;
   int T, d_out, nkb, y_f32;
-  int tiles_m, tiles_n;     // pair kernel
+  int tiles_m, tiles_n;     // not the few-token kernel
 };
 
 // plan: tensor maps, tile choice (host only); run: the launch.
@@ -27,6 +27,7 @@ struct Fp8GemmPlan {
   size_t smem;
   int few;                  // 0: pair kernel; else tokens per tile of the few-token kernel
   int cluster;
+  bool mid;                 // K split over a cluster
   bool f32, empty;
 };
 cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int64_t T, int64_t d_in,
