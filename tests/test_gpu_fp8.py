@@ -125,7 +125,7 @@ def _to_gpu(aq, sa, wq, sw):
 # single tokens, both sides of every tile width and of the kernels' limit;
 # widths of less than a block, off the block grid, with K ranges of a cluster
 SHAPES = [(1, 16, 16), (1, 2048, 144), (2, 128, 128), (15, 400, 272), (16, 1040, 128), (17, 256, 16),
-          (32, 5120, 256), (33, 144, 528), (64, 1168, 384), (65, 2048, 272), (127, 272, 1040),
+          (32, 5120, 256), (33, 144, 528), (48, 1040, 400), (49, 2064, 144), (64, 1168, 384), (65, 2048, 272), (127, 272, 1040),
           (128, 512, 128), (129, 640, 400), (257, 1040, 272), (512, 256, 528), (513, 272, 272),
           (600, 2064, 1552), (769, 128, 16), (1100, 1296, 784),
           # more tiles than CTA pairs, an odd number of K blocks: buffers and stages change places

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(F_THREADS, 2)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   using Smem = FewSmem<N>;
   constexpr int NST = Smem::kStages;
-  constexpr int TCOLS = F_BUFS * N;
+  constexpr int TCOLS = F_BUFS * (N == 48 ? 64 : N);    // a power of two
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   volatile uint32_t* abort_flag = &sm.abort_flag;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(F_THREADS, 2)
         break;
       const float sb = sm.sb[q];
       tc_fence_after();
-      constexpr int CH = N < 32 ? 16 : 32;
+      constexpr int CH = N % 32 != 0 ? 16 : 32;
 #pragma unroll
       for (int c = 0; c < N / CH; ++c) {
         uint32_t r[CH];
@@ -922,11 +922,17 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
   a.y_f32 = f32 ? 1 : 0;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (T <= kFp8FewMaxT) {
-    const int N = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-    const cudaError_t e = N == 16 ? few_attr<16>() : N == 32 ? few_attr<32>() : few_attr<64>();
+    const int N = T <= 16 ? 16 : T <= 32 ? 32 : T <= 48 ? 48 : 64;
+    const cudaError_t e = N == 16   ? few_attr<16>()
+                          : N == 32 ? few_attr<32>()
+                          : N == 48 ? few_attr<48>()
+                                    : few_attr<64>();
     if (e != cudaSuccess) return e;
     p->few = N;
-    p->smem = (N == 16 ? sizeof(FewSmem<16>) : N == 32 ? sizeof(FewSmem<32>) : sizeof(FewSmem<64>)) + 1024;
+    p->smem = 1024 + (N == 16   ? sizeof(FewSmem<16>)
+                      : N == 32 ? sizeof(FewSmem<32>)
+                      : N == 48 ? sizeof(FewSmem<48>)
+                                : sizeof(FewSmem<64>));
     const int tn = static_cast<int>((d_out + 127) / 128);
     // K is split as far as all CTAs run at once, two per SM (sizes that pack
     // into a GPU's groups of SMs; T = 1, 5120 -> 5120, 40 tiles: 1 16.2, 2 10.7,
@@ -1003,7 +1009,10 @@ cudaError_t run_fp8_gemm(const Fp8GemmPlan& p, cudaStream_t stream) {
     cfg.blockDim = dim3(F_THREADS, 1, 1);
     attr[0].val.clusterDim.z = static_cast<unsigned>(p.cluster);
     void (*k)(CUtensorMap, CUtensorMap, Fp8GemmArgs) =
-        p.few == 16 ? fp8_gemm_few_kernel<16> : p.few == 32 ? fp8_gemm_few_kernel<32> : fp8_gemm_few_kernel<64>;
+        p.few == 16   ? fp8_gemm_few_kernel<16>
+        : p.few == 32 ? fp8_gemm_few_kernel<32>
+        : p.few == 48 ? fp8_gemm_few_kernel<48>
+                      : fp8_gemm_few_kernel<64>;
     return cudaLaunchKernelEx(&cfg, k, p.tm_w, p.tm_x, p.a);
   }
   if (p.mid) {
