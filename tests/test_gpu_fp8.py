@@ -125,14 +125,14 @@ def _to_gpu(aq, sa, wq, sw):
 # single tokens, both sides of every tile width and of the kernels' limit;
 # widths of less than a block, off the block grid, with K ranges of a cluster
 SHAPES = [(1, 16, 16), (1, 2048, 144), (2, 128, 128), (15, 400, 272), (16, 1040, 128), (17, 256, 16),
-          (32, 5120, 256), (33, 144, 528), (48, 1040, 400), (49, 2064, 144), (64, 1168, 384), (65, 2048, 272), (127, 272, 1040),
-          (128, 512, 128), (129, 640, 400), (257, 1040, 272), (512, 256, 528), (513, 272, 272),
-          (600, 2064, 1552), (769, 128, 16), (1100, 1296, 784),
+          (32, 5120, 256), (33, 144, 528), (48, 1040, 400), (49, 2064, 144), (64, 1168, 384),
+          (65, 2048, 272), (127, 272, 1040), (128, 512, 128), (129, 640, 400), (257, 1040, 272),
+          (512, 256, 528), (513, 272, 272), (600, 2064, 1552), (769, 128, 16), (1100, 1296, 784),
           # more tiles than CTA pairs, an odd number of K blocks: buffers and stages change places
           (2600, 400, 2064),
-          # K split over clusters of 5, 5, 5, 5, 4, 3 and 2, in even and uneven ranges
-          (66, 1808, 16), (65, 3856, 400), (128, 5120, 256), (129, 4000, 2576), (100, 4112, 7184),
-          (200, 4752, 4624), (260, 6416, 4880)]
+          # K split over clusters, of few-token tiles and of large ones, in even and uneven ranges
+          (66, 1808, 16), (65, 3856, 400), (128, 5120, 256), (129, 1808, 2064), (129, 4000, 2576),
+          (100, 4112, 7184), (200, 4752, 4624), (260, 6416, 4880)]
 
 
 @pytest.mark.parametrize("T,d_in,d_out", SHAPES)
@@ -230,7 +230,7 @@ def test_offsets_past_32_bits(T, ld):
     assert (np.abs(_f64(Y) - y) <= ref.product_tolerance(y, mag, 256, True)).all()
 
 
-@pytest.mark.parametrize("T", [1, 48, 640])
+@pytest.mark.parametrize("T", [1, 48, 640, 4000])
 def test_captured_and_replayed(T):
     rng = _rng(10, T)
     w = fp8.pack_weight(_bf16(0.02 * rng.standard_normal((400, 2048))))
@@ -258,7 +258,7 @@ def test_two_streams():
     rng = _rng(12)
     w = fp8.pack_weight(_bf16(0.02 * rng.standard_normal((1040, 2048))))
     jobs = []
-    for i, T in enumerate((5, 300, 700, 48)):
+    for i, T in enumerate((5, 300, 700, 48, 4000)):
         X = _acts(_rng(13, i), T, 2048)
         ws = torch.empty(fp8.workspace_size(T, w), dtype=torch.uint8, device="cuda")
         Y, Z = (torch.empty(T, 1040, dtype=torch.bfloat16, device="cuda") for _ in range(2))
@@ -278,11 +278,11 @@ def test_split_k_captured_beside_another_stream():
     # clusters that join through shared memory, in a graph and eagerly at once;
     # a token that is not finite touches no other
     rng = _rng(15)
-    w = fp8.pack_weight(_bf16(0.02 * rng.standard_normal((1040, 4112))))
+    w = fp8.pack_weight(_bf16(0.02 * rng.standard_normal((2064, 4112))))
     T = 150
     X, V = _acts(rng, T, 4112), _acts(rng, T, 4112)
     ws, ws2 = (torch.empty(fp8.workspace_size(T, w), dtype=torch.uint8, device="cuda") for _ in range(2))
-    Y, Z, U, R, S = (torch.empty(T, 1040, dtype=torch.bfloat16, device="cuda") for _ in range(5))
+    Y, Z, U, R, S = (torch.empty(T, 2064, dtype=torch.bfloat16, device="cuda") for _ in range(5))
     fp8.linear(X, w, ws, R)
     fp8.linear(V, w, ws, S)
     torch.cuda.synchronize()

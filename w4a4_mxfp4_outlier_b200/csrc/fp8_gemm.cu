@@ -13,13 +13,12 @@
 // Three kernels:
 //  * fp8_gemm_pair_kernel: CTA pairs (cta_group::2), 256 tokens x 256 channels
 //    per tile, persistent.
-//  * fp8_gemm_mid_kernel: for products whose tiles of 256 x 256 would leave most
-//    SMs idle: 128 tokens x 256 channels per CTA, and the CTAs of a cluster split K
-//    and join their sums in the same way.
 //  * fp8_gemm_few_kernel: for few tokens, where reading the weight is the
-//    work: the weight rows are the MMA's M (128 per CTA), the tokens its N
-//    (16 .. 64), and the CTAs of a cluster split K and join their sums through
-//    distributed shared memory, in the order of the ranks.
+//    work, and for small products: the weight rows are the MMA's M (128 per CTA),
+//    the tokens its N (16 .. 64), and the CTAs of a cluster split K and join
+//    their sums through distributed shared memory, in the order of the ranks.
+//  * fp8_gemm_mid_kernel: where tiles of 256 x 256 would leave most SMs idle:
+//    128 tokens x 256 channels per CTA, K split and joined in the same way.
 // Every wait is bounded, as in the other kernels of the library.
 #include <cuda.h>
 
@@ -76,7 +75,8 @@ __global__ void __launch_bounds__(F_THREADS, 2)
   const int C = static_cast<int>(gridDim.z);              // cluster = CTAs along z, one K range each
   const int rank = static_cast<int>(blockIdx.z);
   const int n0 = blockIdx.x * 128;
-  const int nt = args.T;                                  // at most N
+  const int t0 = blockIdx.y * N;
+  const int nt = args.T - t0 < N ? args.T - t0 : N;       // tokens of the tile
   const int kb0 = static_cast<int>(static_cast<int64_t>(args.nkb) * rank / C);
   const int kb1 = static_cast<int>(static_cast<int64_t>(args.nkb) * (rank + 1) / C);
   const int nk = kb1 - kb0;
@@ -141,10 +141,10 @@ __global__ void __launch_bounds__(F_THREADS, 2)
         break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&sm.full[s], N * 128);
-        tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, 0);
+        tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, t0);
         sm.sb[q] = sbi;
         mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
-        bulk_load(sm.sa[q], args.sa + (kb0 + i) * args.ld_sa, sa_bytes, &sm.sa_full[q]);
+        bulk_load(sm.sa[q], args.sa + (kb0 + i) * args.ld_sa + t0, sa_bytes, &sm.sa_full[q]);
       }
       __syncwarp();
     }
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(F_THREADS, 2)
         v[0].x += v[r].x;
         v[0].y += v[r].y;
       }
-      const int64_t at = t * args.ldy + n0 + c;
+      const int64_t at = (t0 + t) * args.ldy + n0 + c;
       if (args.y_f32) {
         *reinterpret_cast<float2*>(static_cast<float*>(args.Y) + at) = v[0];
       } else {
@@ -900,8 +900,13 @@ static int fp8_pair_capacity() {
   return cached[dev];
 }
 
-// Token counts up to this take the few-token kernel.
+// Token counts up to the first take the few-token kernel, and so do products of
+// few tiles of 128 channels x 64 tokens, which it can split eight ways at once
+// (linear(), us, without this rule and with it: 128 x 1024 x 1024 9.6, 7.5;
+// 128 x 4096 x 1024 12.5, 10.1; 384 x 7168 x 512 15.8, 14.5; 128 x 2048 x 2048,
+// 32 tiles, 11.2, 10.6; above 32 tiles 192 x 2048 x 2048 11.7, 14.4).
 constexpr int64_t kFp8FewMaxT = 64;
+constexpr int64_t kFp8FewMaxTiles = 32;
 
 cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int64_t T, int64_t d_in,
                           int64_t d_out, const uint8_t* wq, const float* wscale, void* Y, int64_t ldy,
@@ -921,7 +926,8 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
   a.nkb = static_cast<int>((d_in + kFp8Block - 1) / kFp8Block);
   a.y_f32 = f32 ? 1 : 0;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (T <= kFp8FewMaxT) {
+  const int tn = static_cast<int>((d_out + 127) / 128);
+  if (T <= kFp8FewMaxT || tn * ((T + 63) / 64) <= kFp8FewMaxTiles) {
     const int N = T <= 16 ? 16 : T <= 32 ? 32 : T <= 48 ? 48 : 64;
     const cudaError_t e = N == 16   ? few_attr<16>()
                           : N == 32 ? few_attr<32>()
@@ -933,15 +939,15 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
                       : N == 32 ? sizeof(FewSmem<32>)
                       : N == 48 ? sizeof(FewSmem<48>)
                                 : sizeof(FewSmem<64>));
-    const int tn = static_cast<int>((d_out + 127) / 128);
+    const int ty = static_cast<int>((T + N - 1) / N);
     // K is split as far as all CTAs run at once, two per SM (sizes that pack
     // into a GPU's groups of SMs; T = 1, 5120 -> 5120, 40 tiles: 1 16.2, 2 10.7,
     // 3 9.0, 4 8.8, 6 8.2, 8 11.5 us)
     int C = 1;
     for (const int c : {2, 3, 4, 6, 8})
-      if (tn * c <= 2 * 148 && c <= a.nkb) C = c;
+      if (tn * ty * c <= 2 * 148 && c <= a.nkb) C = c;
     p->cluster = C;
-    p->grid = dim3(tn, 1, C);
+    p->grid = dim3(tn, ty, C);
     if (!make_tmap(&p->tm_w, wq, u8, 1, d_in, d_out, d_in, 128) ||
         !make_tmap(&p->tm_x, aq, u8, 1, d_in, T, d_in, N))
       return cudaErrorInvalidValue;
