@@ -858,16 +858,32 @@ static cudaError_t few_attr() {
   return e;
 }
 
-static cudaError_t mid_attr() {
-  static int done[64] = {0};
+// Clusters of C CTAs of the mid kernel that run at once (C = 2 .. 5: 74, 45, 33, 26);
+// 0 on an error.
+static int mid_capacity(int C) {
+  static int cached[64][H_MAX_C + 1] = {{0}};
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(fp8_gemm_mid_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(MidSmem) + 1024));
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
-  return e;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cached[dev][C] > 0) return cached[dev][C];
+  const size_t smem = sizeof(MidSmem) + 1024;
+  if (cudaFuncSetAttribute(fp8_gemm_mid_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(148, 1, C);
+  cfg.blockDim = dim3(H_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = static_cast<unsigned>(C);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_mid_kernel, &cfg) != cudaSuccess) return 0;
+  cached[dev][C] = n;
+  return n;
 }
 
 static int fp8_pair_capacity() {
@@ -955,22 +971,19 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
   }
   a.tiles_m = static_cast<int>((T + 127) / 128);
   a.tiles_n = static_cast<int>((d_out + 255) / 256);
-  // Where the tiles leave SMs idle, K is split over the CTAs of a cluster.  The
-  // join costs 2 us (two CTAs, few rows) to 6 us (five, 128 rows), a K block
-  // 0.43 us in either kernel, so the split has to spare some.  120 CTAs in
-  // clusters of up to 5 run at once, 140 in clusters of 7 were seen not to.
-  // linear(), us, pair kernel and this one (CTAs of a cluster): 128 x 5120 x 5120
-  // 23.3, 15.1 (5); 256 x 5120 x 5120 24.4, 19.8 (3); 300 x 5120 x 5120 25.0, 25.0
-  // (2); 128 x 13824 x 5120 52.1, 25.0 (5); 384 x 13824 x 5120 57.8, 40.5 (2);
-  // 128 x 2048 x 5120 13.1, 12.2 (5); 128 x 1024 x 1024, which spares 6 blocks,
-  // 9.6, 10.4.
+  // Where the tiles leave SMs idle, K is split over the CTAs of a cluster, as far
+  // as all clusters run at once.  The join costs 2 us (two CTAs, few rows) to 6 us
+  // (five, 128 rows), a K block 0.43 us in either kernel, so the split has to
+  // spare some.  linear(), us, pair kernel and this one (CTAs of a cluster):
+  // 128 x 5120 x 5120 23.3, 15.1 (5); 256 x 5120 x 5120 24.4, 19.8 (3);
+  // 300 x 5120 x 5120 25.0, 22.5 (2); 128 x 13824 x 5120 52.1, 25.0 (5);
+  // 384 x 13824 x 6144 58.5, 42.1 (2); 128 x 2048 x 5120 13.1, 12.2 (5);
+  // 128 x 1024 x 1024, which spares 6 blocks, 9.6, 10.4.
   const int64_t mid_tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
   int C = 1;
   for (int c = 2; c <= H_MAX_C; ++c)
-    if (mid_tiles * c <= 120) C = c;
+    if (mid_tiles <= mid_capacity(c)) C = c;
   if (a.nkb - (a.nkb + C - 1) / C >= 12) {
-    const cudaError_t e = mid_attr();
-    if (e != cudaSuccess) return e;
     p->mid = true;
     p->cluster = C;
     p->grid = dim3(static_cast<unsigned>(mid_tiles), 1, C);
