@@ -371,17 +371,19 @@ w4a4_status w4a4_fp8_pack_weight(const void* W, int64_t ldw, const w4a4_fp8_weig
 
 /* Y[t, n] = sum_b scale_a[b, t] * scale_w[n/128, b] * sum_{p in block b} a[t, p] w[n, p]
  * for w->experts == 1: the sums over a block on the tensor cores, the sum over
- * blocks in float32 in ascending b (few tokens: in up to 8 ascending ranges of
- * b whose sums are then added in order; a function of the shape alone).  The
- * product of the two scales is formed first, in float32.  Y: bf16 [T, d_out]
- * or, with y_f32 != 0, float32; ldy % 8 == 0.  ld_scale as above. */
+ * blocks in float32 in ascending b (where there are few tiles, in up to 8
+ * ascending ranges of b whose sums are then added in order; by a rule on the
+ * shape and the device, so equal calls give equal bits).  The product of the
+ * two scales is formed first, in float32.  Y: bf16 [T, d_out] or, with
+ * y_f32 != 0, float32; ldy % 8 == 0.  ld_scale as above. */
 w4a4_status w4a4_fp8_gemm(const uint8_t* a, const float* scale_a, int64_t ld_scale, int64_t T,
                           const w4a4_fp8_weight* w, void* Y, int64_t ldy, int y_f32, void* stream);
 
 /* Bytes of device workspace w4a4_fp8_linear needs for T tokens of d_in columns. */
 w4a4_status w4a4_fp8_workspace_size(int64_t T, int64_t d_in, size_t* bytes);
 
-/* The layer: w4a4_fp8_quant_act into the workspace, then w4a4_fp8_gemm. */
+/* The layer: w4a4_fp8_quant_act into the workspace, then w4a4_fp8_gemm.  Calls
+ * that may run at the same time need workspaces of their own. */
 w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp8_weight* w,
                             void* workspace, size_t ws_bytes, void* Y, int64_t ldy, int y_f32,
                             void* stream);

@@ -13,7 +13,8 @@ quant_act and pack_weight choose the smallest power of two s with
 max|x| <= 448 s; the product takes any float32 scales.  Every call checks its
 tensors and the status the library returns, runs on the tensors' device and on
 the given stream (default: that device's current stream), and allocates
-nothing unless it says so.
+nothing unless it says so.  Calls that may overlap on the GPU need workspaces
+of their own.
 """
 from __future__ import annotations
 
