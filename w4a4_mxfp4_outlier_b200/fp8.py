@@ -117,14 +117,26 @@ def _ld(t: torch.Tensor) -> int:
 _F8 = (torch.uint8, torch.float8_e4m3fn)
 
 
-@dataclass
+# The records below are frozen: what the library gets of one (sizes, pointers) is
+# taken from its fields when it is made, and none can be assigned after that.  A
+# tensor's own memory can still be exchanged (t.data = ...; t.set_(...); t.resize_(...)),
+# so each call first looks whether the tensors are where they were (0.2 us) and, if
+# one is not, checks and takes everything anew.
+def _put(record, **values):
+    for name, value in values.items():
+        object.__setattr__(record, name, value)
+
+
+@dataclass(frozen=True)
 class Fp8Weight:
     """e4m3 codes [d_out, d_in] with float32 scales [ceil(d_out/128),
     ceil(d_in/128)], or a stack of them with a leading dimension."""
     q: torch.Tensor
     scale: torch.Tensor
-    c: Fp8WeightC = field(init=False, repr=False, compare=False)
     device: torch.device = field(init=False, repr=False, compare=False)
+    d_in: int = field(init=False, repr=False, compare=False)
+    d_out: int = field(init=False, repr=False, compare=False)
+    experts: int = field(init=False, repr=False, compare=False)
 
     def __post_init__(self):
         if self.q.dim() not in (2, 3):
@@ -133,30 +145,52 @@ class Fp8Weight:
         _dense(self.q, _F8, self.q.shape, None, "Fp8Weight q")
         _dense(self.scale, (torch.float32,), lead + (blocks(d_out), blocks(d_in)), self.q.device,
                "Fp8Weight scale")
-        self.device = self.q.device
-        self.d_in, self.d_out, self.experts = int(d_in), int(d_out), int(lead[0]) if lead else 1
-        self.c = Fp8WeightC(self.d_in, self.d_out, self.experts, self.q.data_ptr(), self.scale.data_ptr())
-        self._ref = ctypes.byref(self.c)
+        at = self.q.data_ptr(), self.scale.data_ptr()
+        experts = int(lead[0]) if lead else 1
+        c = Fp8WeightC(int(d_in), int(d_out), experts, *at)
+        _put(self, device=self.q.device, d_in=int(d_in), d_out=int(d_out), experts=experts, _at=at,
+             _by=ctypes.byref(c))
+
+    @property
+    def _ref(self):
+        if (self.q.data_ptr(), self.scale.data_ptr()) != self._at:
+            self.__post_init__()
+        return self._by
+
+    @property
+    def c(self) -> Fp8WeightC:
+        """The C record, a copy."""
+        return Fp8WeightC.from_buffer_copy(self._ref._obj)
 
 
-@dataclass
+@dataclass(frozen=True)
 class Fp8Act:
     """Quantised activations: q uint8 [T, d], scale float32 [ceil(d/128), ld]
     (token t and block b at [b, t]; ld is T rounded up to 4, or more)."""
     q: torch.Tensor
     scale: torch.Tensor
+    device: torch.device = field(init=False, repr=False, compare=False)
+    T: int = field(init=False, repr=False, compare=False)
+    d: int = field(init=False, repr=False, compare=False)
+    ld: int = field(init=False, repr=False, compare=False)
 
     def __post_init__(self):
         if self.q.dim() != 2 or self.scale.dim() != 2:
             raise W4A4Error(ERR_INVALID_ARG, "Fp8Act: q and scale are 2-D")
-        self.T, self.d = (int(n) for n in self.q.shape)
-        self.ld, self.device = int(self.scale.shape[1]), self.q.device
-        if self.ld < (self.T + 3) // 4 * 4:
-            raise W4A4Error(ERR_INVALID_ARG, f"Fp8Act: no room for {self.T} scales in rows of {self.ld}")
-        if self.device.type == "cuda":
-            _dense(self.q, _F8, (self.T, self.d), self.device, "Fp8Act q")
-            _dense(self.scale, (_F32,), (blocks(self.d), self.ld), self.device, "Fp8Act scale")
-        self._args = self.q.data_ptr(), self.scale.data_ptr(), self.ld
+        (T, d), ld, device = (int(n) for n in self.q.shape), int(self.scale.shape[1]), self.q.device
+        if ld < (T + 3) // 4 * 4:
+            raise W4A4Error(ERR_INVALID_ARG, f"Fp8Act: no room for {T} scales in rows of {ld}")
+        if device.type == "cuda":
+            _dense(self.q, _F8, (T, d), device, "Fp8Act q")
+            _dense(self.scale, (_F32,), (blocks(d), ld), device, "Fp8Act scale")
+        at = self.q.data_ptr(), self.scale.data_ptr()
+        _put(self, device=device, T=T, d=d, ld=ld, _at=at, _arg=(*at, ld))
+
+    @property
+    def _args(self):
+        if (self.q.data_ptr(), self.scale.data_ptr()) != self._at:
+            self.__post_init__()
+        return self._arg
 
 
 def alloc_act(T: int, d: int, device="cuda") -> Fp8Act:
@@ -165,10 +199,11 @@ def alloc_act(T: int, d: int, device="cuda") -> Fp8Act:
 
 
 def quant_act(X: torch.Tensor, out: Fp8Act, stream=None) -> Fp8Act:
+    args = out._args
     T, ld = _rows_in(X, out.d, out.device, "fp8.quant_act")
     if T != out.T:
         raise W4A4Error(ERR_INVALID_ARG, f"fp8.quant_act: X has {T} rows, out {out.T}")
-    _run(out.device, stream, "fp8.quant_act", _quant_act, X.data_ptr(), T, out.d, ld, *out._args)
+    _run(out.device, stream, "fp8.quant_act", _quant_act, X.data_ptr(), T, out.d, ld, *args)
     return out
 
 
@@ -190,11 +225,12 @@ def pack_weight(W: torch.Tensor, stream=None) -> Fp8Weight:
 
 def gemm(act: Fp8Act, w: Fp8Weight, Y: torch.Tensor, stream=None) -> torch.Tensor:
     """Y = act @ w^T, bf16 or float32 by Y's type."""
+    args, ref = act._args, w._ref
     if act.d != w.d_in or act.device != w.device:
         raise W4A4Error(ERR_INVALID_ARG, f"fp8.gemm: activations of {act.d} columns on {act.device}, weight "
                                          f"of {w.d_in} on {w.device}")
     ld, f32 = _rows_out(Y, act.T, w.d_out, w.device, "fp8.gemm")
-    _run(w.device, stream, "fp8.gemm", _gemm, *act._args, act.T, w._ref, Y.data_ptr(), ld, f32)
+    _run(w.device, stream, "fp8.gemm", _gemm, *args, act.T, ref, Y.data_ptr(), ld, f32)
     return Y
 
 
@@ -207,10 +243,10 @@ def workspace_size(T: int, w: Fp8Weight) -> int:
 def linear(X: torch.Tensor, w: Fp8Weight, workspace: torch.Tensor, Y: torch.Tensor,
            stream=None) -> torch.Tensor:
     """Y = quant_act(X) @ w^T, bf16 or float32 by Y's type."""
-    dev = w.device
+    ref, dev = w._ref, w.device
     T, ldx = _rows_in(X, w.d_in, dev, "fp8.linear")
     ldy, f32 = _rows_out(Y, T, w.d_out, dev, "fp8.linear")
     _bytes(workspace, dev, "fp8.linear")
-    _run(dev, stream, "fp8.linear", _linear, X.data_ptr(), T, ldx, w._ref, workspace.data_ptr(),
+    _run(dev, stream, "fp8.linear", _linear, X.data_ptr(), T, ldx, ref, workspace.data_ptr(),
          workspace.nbytes, Y.data_ptr(), ldy, f32)
     return Y
