@@ -445,7 +445,10 @@ __global__ void __launch_bounds__(H_THREADS, 1)
       mbar_wait_bounded(&sm.acc_full[b], (i >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
       __syncwarp();
       tc_fence_after();
-      if (qi == H_SA_GROUP - 1 && lane == 0) mbar_arrive(&sm.sa_empty[q]);   // (all lanes have read theirs)
+      if (qi == H_SA_GROUP - 1) {                        // (all lanes have read theirs)
+        if (lane == 0) mbar_arrive(&sm.sa_empty[q]);
+        __syncwarp();                                    // tensor memory is read by a converged warp
+      }
       const float2 m2 = make_float2(m, m);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -761,6 +764,7 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         if (qi == Q_SA_GROUP - 1 || kb + 1 == nkb) {     // (all lanes have read their scale)
           if (lane == 0) mbar_arrive(&sm.sa_empty[q]);
           ++grp;
+          __syncwarp();                                  // tensor memory is read by a converged warp
         }
       };
       for (int kb = 0; kb < nkb; ++kb, ++g) {

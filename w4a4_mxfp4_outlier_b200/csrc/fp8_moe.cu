@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_const
     if (t % 4 == 0)
       for (int kb = rank * 8 + (tid >> 4); kb - odd < nb; kb += R_CTAS * 8)
         fp8_quant_rows4(a.X, a.T, a.d, a.ldx, a.xq, a.xs, a.ld_x, t, kb);
+    __syncwarp();
     cluster_wait();
   } else {
     const int e_end = (rank + 1) * epc < a.E ? (rank + 1) * epc : a.E;
@@ -282,17 +283,23 @@ struct MoeSmem {
   uint32_t abort_flag;
 };
 
-// named barrier over `nthreads` threads that also tells all of them whether
-// any had a non-zero pred
-__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, uint32_t pred) {
+// The barrier of the 128 finishing threads.  Named barriers are instructions of
+// whole warps, and single lanes have work of their own before many of them.
+__device__ __forceinline__ void finish_sync() {
+  __syncwarp();
+  named_bar_sync(1, 128);
+}
+// The same, which also tells all of them whether any had a non-zero pred.
+__device__ __forceinline__ bool finish_any(uint32_t pred) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
       "bar.red.or.pred p, %2, %3, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(pred), "r"(id), "r"(nthreads)
+      : "r"(pred), "r"(1u), "r"(128u)
       : "memory");
   return r != 0;
 }
@@ -335,13 +342,13 @@ __device__ __forceinline__ float moe_gelu(float y) {
 // After all 128 finishing threads' writes: counts one arrival; true for all of
 // them if it was the last of `all`, whose earlier writes they may then read.
 __device__ __forceinline__ bool moe_last_arrival(int* counter, int all, int* last, int tid) {
-  named_bar_sync(1, 128);
+  finish_sync();
   if (tid == 0) {
     __threadfence();
     *last = atomicAdd(counter, 1) == all - 1;
     __threadfence();
   }
-  named_bar_sync(1, 128);
+  finish_sync();
   return *last != 0;
 }
 
@@ -390,7 +397,7 @@ __device__ __forceinline__ void moe_finish_h(const MoeArgs& a, uint32_t (&amax)[
       const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h[i]) & 0x7FFFFFFFu);
       if ((tid & 31) == 0) amax[buf][i][tid >> 5] = w;
     }
-    named_bar_sync(1, 128);
+    finish_sync();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (p0 + i < m) {
@@ -664,6 +671,9 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         for (int kb = k0 + lane; kb < k1 && got; kb += 32)
           got = counter_wait_bounded(a.ready + un.ex * nkb_f + kb, 1, abort_flag, DEVERR_TIMEOUT_PRODUCER);
         if (!__all_sync(0xFFFFFFFFu, got)) break;
+        // every lane acquired other blocks' flags, one lane issues all copies: the
+        // vote alone does not order the one behind the others
+        __syncwarp();
         fence_proxy_async_global();
       }
       for (int kb = k0; kb < k1; ++kb, ++it) {
@@ -814,19 +824,19 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     // ============================ finishing ===============================
     // What follows a unit's sums, while the next unit's are made.  The four
     // warps agree at their barriers on whether one of them gave up
-    // (named_bar_or), so none is left waiting for another.
+    // (finish_any), so none is left waiting for another.
     const int tid = threadIdx.x - 384;
     for (uint32_t u = 0;; ++u) {
       const int us = static_cast<int>(u % M_UNITS);
       bool ok = warp_wait_bounded(&sm.unit_full[us], (u / M_UNITS) & 1u, abort_flag,
                                   DEVERR_TIMEOUT_EPILOGUE);
-      if (named_bar_or(1, 128, !ok)) break;
+      if (finish_any(!ok)) break;
       const MoeUnit un = sm.unit[us];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.unit_empty[us]);
       if (un.kind == 2) break;
       ok = warp_wait_bounded(&sm.sums_full, u & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
-      if (named_bar_or(1, 128, !ok)) break;
+      if (finish_any(!ok)) break;
       const int e = sm.act_e[un.ex];
       const int off = sm.off[e];
       const int m = __popcll(sm.mask[e]);
@@ -854,7 +864,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
             moe_finish_h<true>(a, sm.amax, off, m, un.blk, s_up, src, 0, tid);
           } else {
             moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk, s_up, src, 0, tid);
-            named_bar_sync(1, 128);
+            finish_sync();
             if (2 * un.blk + 1 < nkb_f)
               moe_finish_h<false>(a, sm.amax, off, m, 2 * un.blk + 1, s_up, src, 128, tid);
           }
@@ -863,7 +873,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
             if (lane == 0) mbar_arrive(&sm.sums_empty);
           }
           fence_proxy_async_global();
-          named_bar_sync(1, 128);
+          finish_sync();
           if (tid == 0) {
             __threadfence();
             int* flag = a.ready + un.ex * nkb_f + (kGated ? un.blk : 2 * un.blk);
@@ -881,7 +891,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.sums_empty);
-        named_bar_sync(1, 128);
+        finish_sync();
         if (tid == 0) {
           __threadfence();
           atomicAdd(a.dn_done, 1);
@@ -893,7 +903,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     bool done = *abort_flag == 0u;
     if (done && tid == 0)
       done = counter_wait_bounded(a.dn_done, dn_tiles * n_act * s_dn, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
-    if (!named_bar_or(1, 128, !done))
+    if (!finish_any(!done))
       moe_combine(a, sm.row_of, s_dn, blockIdx.x * 128 + tid, gridDim.x * 128);
   }
 
