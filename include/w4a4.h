@@ -392,7 +392,7 @@ w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp
  * A mixture-of-experts layer for a few tokens (T <= 64), whole, in two
  * kernels: router, selection, the chosen experts' two projections and the
  * weighted sum.
- *   l[t, e] = sum_j x[t, j] router[e, j]              (float32)
+ *   l[t, e] = sum_j x[t, j] router[e, j]              (summed in 64 bits)
  *   E_t     = the top_k experts of largest l, equal ones by lower index, NaN last
  *   w[t, e] = exp(l[t, e]) / sum exp(l[t, .]), the sum over E_t (renorm != 0)
  *             or over all experts
