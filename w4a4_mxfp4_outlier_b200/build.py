@@ -26,7 +26,7 @@ SOURCES = ["libw4a4.cu"]
 HEADERS = ["w4a4_device.cuh", "w4a4_internal.h", "w4a4_api.cu", "calib.cu", "prep.cu", "prep_block.cu",
            "pack.cu", "gemm.cu", "noalloc.cu",
            "checkpoint.cu", "metrics.cu", "ffn.cu",
-           "fp8_device.cuh", "fp8_internal.h", "fp8_quant.cu", "fp8_gemm.cu", "fp8_moe.cu",
+           "fp8_device.cuh", "fp8_internal.h", "fp8_rules.h", "fp8_quant.cu", "fp8_gemm.cu", "fp8_moe.cu",
            "fp8_api.cu"]
 
 

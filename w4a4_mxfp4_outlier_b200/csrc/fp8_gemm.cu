@@ -24,6 +24,7 @@
 
 #include "fp8_device.cuh"
 #include "fp8_internal.h"
+#include "fp8_rules.h"
 
 namespace w4a4 {
 
@@ -33,6 +34,7 @@ namespace w4a4 {
 constexpr int F_THREADS = 224;                // weights, MMA, 4 epilogue, activations
 constexpr int F_W_BYTES = 128 * 128;          // weight rows x bytes of one K block
 constexpr int F_BUFS = 4;                     // accumulators in tensor memory
+constexpr int F_PER_SM = 2;                   // CTAs that run on an SM
 
 template <int N>
 struct FewSmem {
@@ -59,7 +61,7 @@ struct FewSmem {
 };
 
 template <int N>
-__global__ void __launch_bounds__(F_THREADS, 2)
+__global__ void __launch_bounds__(F_THREADS, F_PER_SM)
     fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w,
                         const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ Fp8GemmArgs args) {
@@ -67,6 +69,8 @@ __global__ void __launch_bounds__(F_THREADS, 2)
   using Smem = FewSmem<N>;
   constexpr int NST = Smem::kStages;
   constexpr int TCOLS = F_BUFS * (N == 48 ? 64 : N);    // a power of two
+  static_assert(F_PER_SM * TCOLS <= 512 && F_PER_SM * (sizeof(Smem) + 2048) <= 228 * 1024,
+                "F_PER_SM CTAs fit an SM");
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   volatile uint32_t* abort_flag = &sm.abort_flag;
@@ -849,17 +853,44 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+// Clusters of c CTAs of the few-token kernel that run at once, for every c of
+// kFewSplits, once per device.
 template <int N>
-static cudaError_t few_attr() {
-  static int done[64] = {0};
+static cudaError_t few_fits(const int** fits) {
+  static int cached[64][kFewMaxSplit + 1] = {{0}};      // [0]: filled
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int* n = cached[dev];
+  *fits = n;
+  if (n[0]) return cudaSuccess;
+  const size_t smem = sizeof(FewSmem<N>) + 1024;
   e = cudaFuncSetAttribute(fp8_gemm_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(FewSmem<N>) + 1024));
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
-  return e;
+                           static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(F_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int counted = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&counted, fp8_gemm_few_kernel<N>, F_THREADS, smem);
+  if (e != cudaSuccess) return e;
+  for (const int c : kFewSplits) {
+    attr[0].val.clusterDim.z = static_cast<unsigned>(c);
+    cfg.gridDim = dim3(148, 1, c);
+    int fit = 0;
+    e = cudaOccupancyMaxActiveClusters(&fit, fp8_gemm_few_kernel<N>, &cfg);
+    if (e != cudaSuccess) return e;
+    n[c] = fp8_clusters_that_fit(fit, counted, F_PER_SM);
+  }
+  n[0] = 1;
+  return cudaSuccess;
 }
 
 // Clusters of C CTAs of the mid kernel that run at once (C = 2 .. 5: 74, 45, 33, 26);
@@ -921,7 +952,7 @@ static int fp8_pair_capacity() {
 }
 
 // Token counts up to the first take the few-token kernel, and so do products of
-// few tiles of 128 channels x 64 tokens, which it can split eight ways at once
+// few tiles of 128 channels x 64 tokens, which it can split six or eight ways at once
 // (linear(), us, without this rule and with it: 128 x 1024 x 1024 9.6, 7.5;
 // 128 x 4096 x 1024 12.5, 10.1; 384 x 7168 x 512 15.8, 14.5; 128 x 2048 x 2048,
 // 32 tiles, 11.2, 10.6; above 32 tiles 192 x 2048 x 2048 11.7, 14.4).
@@ -949,10 +980,11 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
   const int tn = static_cast<int>((d_out + 127) / 128);
   if (T <= kFp8FewMaxT || tn * ((T + 63) / 64) <= kFp8FewMaxTiles) {
     const int N = T <= 16 ? 16 : T <= 32 ? 32 : T <= 48 ? 48 : 64;
-    const cudaError_t e = N == 16   ? few_attr<16>()
-                          : N == 32 ? few_attr<32>()
-                          : N == 48 ? few_attr<48>()
-                                    : few_attr<64>();
+    const int* fits = nullptr;
+    const cudaError_t e = N == 16   ? few_fits<16>(&fits)
+                          : N == 32 ? few_fits<32>(&fits)
+                          : N == 48 ? few_fits<48>(&fits)
+                                    : few_fits<64>(&fits);
     if (e != cudaSuccess) return e;
     p->few = N;
     p->smem = 1024 + (N == 16   ? sizeof(FewSmem<16>)
@@ -960,12 +992,8 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
                       : N == 48 ? sizeof(FewSmem<48>)
                                 : sizeof(FewSmem<64>));
     const int ty = static_cast<int>((T + N - 1) / N);
-    // K is split as far as all CTAs run at once, two per SM (sizes that pack
-    // into a GPU's groups of SMs; T = 1, 5120 -> 5120, 40 tiles: 1 16.2, 2 10.7,
-    // 3 9.0, 4 8.8, 6 8.2, 8 11.5 us)
-    int C = 1;
-    for (const int c : {2, 3, 4, 6, 8})
-      if (tn * ty * c <= 2 * 148 && c <= a.nkb) C = c;
+    // (T = 1, 5120 -> 5120, 40 tiles: 1 16.2, 2 10.7, 3 9.0, 4 8.8, 6 8.2, 8 11.5 us)
+    const int C = fp8_few_split(static_cast<int64_t>(tn) * ty, a.nkb, fits);
     p->cluster = C;
     p->grid = dim3(tn, ty, C);
     if (!make_tmap(&p->tm_w, wq, u8, 1, d_in, d_out, d_in, 128) ||
