@@ -18,6 +18,7 @@ of their own.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass, field
 
@@ -66,6 +67,17 @@ def _run(device: torch.device, stream, what: str, fn, *args):
             st = fn(*args, s)
     if st != OK:
         _check(st, what)
+
+
+def _allocating(device: torch.device, stream):
+    """Context in which new tensors are `stream`'s: memory freed on the current
+    stream, whose work there may not have run yet, must not be written by another."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(s, device=device) if s else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _dense(t: torch.Tensor, dtypes, shape, device, what: str):
@@ -208,7 +220,8 @@ def quant_act(X: torch.Tensor, out: Fp8Act, stream=None) -> Fp8Act:
 
 
 def pack_weight(W: torch.Tensor, stream=None) -> Fp8Weight:
-    """Quantises W, bf16 [d_out, d_in] or dense [experts, d_out, d_in]; allocates the result."""
+    """Quantises W, bf16 [d_out, d_in] or dense [experts, d_out, d_in]; allocates the
+    result, on `stream` where one is given."""
     if W.dim() == 3:
         _dense(W, (torch.bfloat16,), W.shape, None, "fp8.pack_weight")
         ldw = W.shape[2]
@@ -216,9 +229,10 @@ def pack_weight(W: torch.Tensor, stream=None) -> Fp8Weight:
         _rows_bf16(W, "fp8.pack_weight")
         ldw = _ld(W)
     d_out, d_in = W.shape[-2:]
-    w = Fp8Weight(torch.empty(W.shape, dtype=torch.uint8, device=W.device),
-                  torch.empty(tuple(W.shape[:-2]) + (blocks(d_out), blocks(d_in)), dtype=torch.float32,
-                              device=W.device))
+    with _allocating(W.device, stream):
+        w = Fp8Weight(torch.empty(W.shape, dtype=torch.uint8, device=W.device),
+                      torch.empty(tuple(W.shape[:-2]) + (blocks(d_out), blocks(d_in)), dtype=torch.float32,
+                                  device=W.device))
     _run(W.device, stream, "fp8.pack_weight", _pack_weight, W.data_ptr(), ldw, w._ref)
     return w
 
