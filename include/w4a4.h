@@ -495,6 +495,9 @@ w4a4_status w4a4_last_error(void* stream, int clear, uint32_t* bits);
  * restore normal operation.  INVALID_ARG for an unknown mask bit or a limit
  * above the default. */
 #define W4A4_FAULT_PREP_SKIP_LOADS 1u
+/* Products and expert layers enqueued while it is set (on any device) copy no
+ * activation tiles: the waits for them run out and the calls end like that. */
+#define W4A4_FAULT_FP8_SKIP_ACTS 4u
 w4a4_status w4a4_test_fault(uint32_t mask, uint64_t wait_limit_ns);
 
 /* Number of streaming multiprocessors of the current device (used to size

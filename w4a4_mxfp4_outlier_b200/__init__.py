@@ -99,6 +99,7 @@ _error_sums = _sig("w4a4_error_sums", _st, _vp, _i64, _vp, _i64, _i64, _i64, _vp
 _last_error = _sig("w4a4_last_error", _st, _vp, ctypes.c_int, ctypes.POINTER(ctypes.c_uint32))
 _test_fault = _sig("w4a4_test_fault", _st, ctypes.c_uint32, ctypes.c_uint64)
 FAULT_PREP_SKIP_LOADS = 1           # W4A4_FAULT_PREP_SKIP_LOADS
+FAULT_FP8_SKIP_ACTS = 4             # W4A4_FAULT_FP8_SKIP_ACTS
 
 EXPORTED = [
     "w4a4_abi_version", "w4a4_status_string", "w4a4_num_sms", "w4a4_get_dims",
@@ -389,8 +390,9 @@ def load_packed(path: str, device="cuda", stream=None) -> PackedWeight:
 
 def test_fault(mask: int, wait_limit_ns: int = 0):
     """Failure-detection test hook (w4a4_test_fault): shorten the device wait
-    limit and make the prep producer skip its copies; test_fault(0, 0)
-    restores normal operation."""
+    limit and make the prep producer (FAULT_PREP_SKIP_LOADS) or the e4m3
+    products and the expert layer (FAULT_FP8_SKIP_ACTS) skip their copies of
+    activations; test_fault(0, 0) restores normal operation."""
     _check(_test_fault(mask, wait_limit_ns), "test_fault")
 
 

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(F_THREADS, F_PER_SM)
         break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&sm.full[s], N * 128);
-        tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, t0);
+        if (!args.no_acts) tma_load_2d(sm.stage[s] + F_W_BYTES, &tm_x, &sm.full[s], (kb0 + i) * 128, t0);
         sm.sb[q] = sbi;
         mbar_arrive_expect_tx(&sm.sa_full[q], sa_bytes);
         bulk_load(sm.sa[q], args.sa + (kb0 + i) * args.ld_sa + t0, sa_bytes, &sm.sa_full[q]);
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(H_THREADS, 1)
           break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&sm.full[s], H_STAGE_BYTES);
-          tma_load_2d(sm.stage[s], &tm_x, &sm.full[s], (kb0 + i) * 128, m0);
+          if (!args.no_acts) tma_load_2d(sm.stage[s], &tm_x, &sm.full[s], (kb0 + i) * 128, m0);
           tma_load_2d(sm.stage[s] + H_X_BYTES, &tm_w, &sm.full[s], (kb0 + i) * 128, n0);
         }
         __syncwarp();
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
           if (elect_one()) {
             const uint32_t full_leader = mapa_shared(smem_u32(&sm.full[s]), 0);
             if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Q_STAGE_BYTES);
-            tma_load_2d_pair(sm.stage[s], &tm_x, full_leader, kb * 128, m_rows);
+            if (!args.no_acts) tma_load_2d_pair(sm.stage[s], &tm_x, full_leader, kb * 128, m_rows);
             tma_load_2d_pair(sm.stage[s] + Q_HALF, &tm_w, full_leader, kb * 128, n_rows);
           }
           __syncwarp();
@@ -976,6 +976,7 @@ cudaError_t plan_fp8_gemm(const uint8_t* aq, const float* sa, int64_t ld_sa, int
   a.d_out = static_cast<int>(d_out);
   a.nkb = static_cast<int>((d_in + kFp8Block - 1) / kFp8Block);
   a.y_f32 = f32 ? 1 : 0;
+  a.no_acts = (host_fault_mask() & FAULT_FP8_SKIP_ACTS) != 0u;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const int tn = static_cast<int>((d_out + 127) / 128);
   if (T <= kFp8FewMaxT || tn * ((T + 63) / 64) <= kFp8FewMaxTiles) {

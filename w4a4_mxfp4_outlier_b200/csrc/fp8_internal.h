@@ -16,6 +16,7 @@ struct Fp8GemmArgs {
   void* Y;
   int64_t ld_sa, ldy;
   int T, d_out, nkb, y_f32;
+  int no_acts;              // failure-detection test hook: copy no activation tiles
   int tiles_m, tiles_n;     // not the few-token kernel
 };
 
@@ -57,6 +58,7 @@ struct MoeArgs {
   int32_t *up_done, *ready, *dn_done, *ticket;
   int64_t ld_x, pairs;
   int T, d, ff, E, top_k, renorm, y_f32, ncounters, most_up, most_dn;
+  int no_acts;                      // failure-detection test hook: copy no activation tiles
 };
 struct MoeLayout {
   int64_t pairs, ld_x, up_done, ready, dn_done, ticket, ncounters;

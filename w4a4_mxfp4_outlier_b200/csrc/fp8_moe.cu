@@ -710,8 +710,9 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         }
         if (elect_one()) {
           mbar_arrive_expect_tx(&sm.full[s], N * 128);
-          tma_load_2d(sm.stage[s] + M_W_BYTES, un.kind == 0 ? &tm_xq : &tm_hq, &sm.full[s], kb * 128,
-                      off);
+          if (!a.no_acts)
+            tma_load_2d(sm.stage[s] + M_W_BYTES, un.kind == 0 ? &tm_xq : &tm_hq, &sm.full[s], kb * 128,
+                        off);
           bulk_load(sm.sa[q], sa + kb * ld, sa_bytes, &sm.sa_full[q]);
         }
         __syncwarp();
@@ -1022,6 +1023,7 @@ cudaError_t plan_moe(const MoeArgs& a, int64_t E, const uint8_t* gate, const uin
                      const uint8_t* down, bool gated, MoePlan* p) {
   memset(p, 0, sizeof(*p));
   p->a = a;
+  p->a.no_acts = (host_fault_mask() & FAULT_FP8_SKIP_ACTS) != 0u;
   p->gated = gated;
   p->n = a.T <= 16 ? 16 : a.T <= 32 ? 32 : 64;
   p->ctas = device_num_sms();

@@ -1,6 +1,7 @@
 // C-ABI entry points of libw4a4 (declared in include/w4a4.h): argument
 // validation, workspace layout and kernel launches.  No entry point
 // allocates device memory.
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 
@@ -24,6 +25,9 @@ bool pdl_enabled() {
   }
   return on == 1;
 }
+
+static std::atomic<uint32_t> g_host_fault_mask{0u};
+uint32_t host_fault_mask() { return g_host_fault_mask.load(std::memory_order_relaxed); }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -307,7 +311,8 @@ w4a4_status w4a4_linear_host(const void* X_host, int64_t T, const w4a4_packed_we
 }
 
 w4a4_status w4a4_test_fault(uint32_t mask, uint64_t wait_limit_ns) {
-  if ((mask & ~static_cast<uint32_t>(FAULT_PREP_SKIP_LOADS)) != 0u) return W4A4_ERR_INVALID_ARG;
+  if ((mask & ~static_cast<uint32_t>(FAULT_PREP_SKIP_LOADS | FAULT_FP8_SKIP_ACTS)) != 0u)
+    return W4A4_ERR_INVALID_ARG;
   const uint64_t limit = wait_limit_ns == 0 ? kWaitLimitNs : wait_limit_ns;
   if (limit > kWaitLimitNs) return W4A4_ERR_INVALID_ARG;
   cudaError_t e = cudaDeviceSynchronize();
@@ -315,6 +320,7 @@ w4a4_status w4a4_test_fault(uint32_t mask, uint64_t wait_limit_ns) {
   e = cudaMemcpyToSymbol(g_wait_limit_ns, &limit, sizeof(limit));
   if (e != cudaSuccess) return W4A4_ERR_CUDA;
   e = cudaMemcpyToSymbol(g_fault_mask, &mask, sizeof(mask));
+  if (e == cudaSuccess) g_host_fault_mask.store(mask);
   return from_cuda(e);
 }
 
