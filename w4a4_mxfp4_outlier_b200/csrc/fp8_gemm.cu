@@ -449,10 +449,7 @@ __global__ void __launch_bounds__(H_THREADS, 1)
       mbar_wait_bounded(&sm.acc_full[b], (i >> 1) & 1u, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
       __syncwarp();
       tc_fence_after();
-      if (qi == H_SA_GROUP - 1) {                        // (all lanes have read theirs)
-        if (lane == 0) mbar_arrive(&sm.sa_empty[q]);
-        __syncwarp();                                    // tensor memory is read by a converged warp
-      }
+      if (qi == H_SA_GROUP - 1) mbar_arrive_lane0(&sm.sa_empty[q], lane);   // (all lanes have read theirs)
       const float2 m2 = make_float2(m, m);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -766,9 +763,8 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
         __syncwarp();
         tc_fence_after();
         if (qi == Q_SA_GROUP - 1 || kb + 1 == nkb) {     // (all lanes have read their scale)
-          if (lane == 0) mbar_arrive(&sm.sa_empty[q]);
+          mbar_arrive_lane0(&sm.sa_empty[q], lane);
           ++grp;
-          __syncwarp();                                  // tensor memory is read by a converged warp
         }
       };
       for (int kb = 0; kb < nkb; ++kb, ++g) {
