@@ -405,7 +405,9 @@ w4a4_status w4a4_fp8_linear(const void* X, int64_t T, int64_t ldx, const w4a4_fp
  * sizes, the number of experts chosen and the device's SM count; results do
  * not depend on timing.
  * A token whose x holds an infinity or a NaN gets NaN in all of y (and any
- * valid expert indexes); other tokens are not affected.
+ * valid expert indexes).  Nothing of it enters other tokens' sums; but since
+ * the split of K follows the number of experts that all tokens chose together,
+ * a token's y may differ in its last bits with the tokens beside it.
  * ------------------------------------------------------------------------ */
 typedef enum w4a4_moe_act { W4A4_MOE_GELU = 0, W4A4_MOE_SILU_GATED = 1 } w4a4_moe_act;
 
