@@ -70,24 +70,33 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// acc0 += x . w0, acc1 += x . w1 over 8 columns, in four sums each (a chain of
-// 64-bit FMAs waits for each one's result).  The selection is the layer's one
-// discontinuous step: two logits closer than a float32 sum's rounding would
-// change places, and with them whole experts.  So logits are summed in 64
-// bits, where the products of bf16 numbers are exact and their sums nearly
-// always are.  (Against float32 sums: 1 token, 64 experts of 2048 columns 25.9 ->
-// 26.6 us for the layer; 64 tokens, 512 experts of 2048 columns 219 -> 237.)
-__device__ __forceinline__ void dot8(const uint4& x, const uint4& w0, const uint4& w1, double (&acc0)[4],
-                                     double (&acc1)[4]) {
+// acc0 += x . w0 and, where there are two experts, acc1 += x . w1 over 8 columns,
+// in four sums each (a chain of 64-bit FMAs waits for each one's result).  The
+// selection is the layer's one discontinuous step: two logits closer than a
+// float32 sum's rounding would change places, and with them whole experts.  So
+// logits are summed in 64 bits, where the products of bf16 numbers are exact
+// and their sums nearly always are.  Layer, us, against float32 sums: 1 token, 6 of
+// 64 experts of 2048 x 1024 25.9, 25.8; 16 tokens, 8 of 128 of 2048 x 768 74.2,
+// 77.0; 64 tokens, 16 of 512 of 2048 x 256 219, 238.  The conversions bound it there;
+// moving the bits into a double's fields instead was no faster.
+__device__ __forceinline__ void dot8(const uint4& x, const uint4& w0, const uint4& w1, bool two,
+                                     double (&acc0)[4], double (&acc1)[4]) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, as[4] = {w0.x, w0.y, w0.z, w0.w},
                  bs[4] = {w1.x, w1.y, w1.z, w1.w};
+  double lo[4], hi[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const double lo = bf16_lo_to_f32(xs[i]), hi = bf16_hi_to_f32(xs[i]);
-    acc0[i] = fma(lo, static_cast<double>(bf16_lo_to_f32(as[i])), acc0[i]);
-    acc1[i] = fma(lo, static_cast<double>(bf16_lo_to_f32(bs[i])), acc1[i]);
-    acc0[i] = fma(hi, static_cast<double>(bf16_hi_to_f32(as[i])), acc0[i]);
-    acc1[i] = fma(hi, static_cast<double>(bf16_hi_to_f32(bs[i])), acc1[i]);
+    lo[i] = bf16_lo_to_f32(xs[i]);
+    hi[i] = bf16_hi_to_f32(xs[i]);
+    acc0[i] = fma(lo[i], static_cast<double>(bf16_lo_to_f32(as[i])), acc0[i]);
+    acc0[i] = fma(hi[i], static_cast<double>(bf16_hi_to_f32(as[i])), acc0[i]);
+  }
+  if (two) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc1[i] = fma(lo[i], static_cast<double>(bf16_lo_to_f32(bs[i])), acc1[i]);
+      acc1[i] = fma(hi[i], static_cast<double>(bf16_hi_to_f32(bs[i])), acc1[i]);
+    }
   }
 }
 
@@ -153,7 +162,7 @@ __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_const
           x[u] = *reinterpret_cast<const uint4*>(xr + c0 + 256 * u);
         }
 #pragma unroll
-        for (int u = 0; u < n; ++u) dot8(x[u], w0[u], w1[u], sum0, sum1);
+        for (int u = 0; u < n; ++u) dot8(x[u], w0[u], w1[u], two, sum0, sum1);
       };
       int c = 256 * s_lo + 8 * lane;
       for (; c + 256 * (U - 1) < c_end; c += 256 * U) step(c, Steps<U>());
