@@ -5,6 +5,12 @@
 
 namespace w4a4 {
 
+// Failure-detection test hook (w4a4_test_fault), beside the prep producer's bit:
+// the products and the expert kernel copy no activation tiles, so that the waits
+// for them run out.  Seen by the host, which hands it to the kernels as an argument.
+enum : uint32_t { FAULT_FP8_SKIP_ACTS = 1u << 2 };
+uint32_t host_fault_mask();       // the mask last given to w4a4_test_fault
+
 cudaError_t launch_fp8_quant_act(const void* X, int64_t T, int64_t d, int64_t ldx, uint8_t* q,
                                  float* scale, int64_t ld_scale, cudaStream_t stream);
 cudaError_t launch_fp8_pack_weight(const void* W, int64_t ldw, int64_t rows, int64_t cols,

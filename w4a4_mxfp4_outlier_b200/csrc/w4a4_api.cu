@@ -5,6 +5,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "fp8_internal.h"
 #include "w4a4.h"
 #include "w4a4_internal.h"
 

@@ -33,9 +33,8 @@ static __device__ uint64_t g_wait_limit_ns = kWaitLimitNs;
 
 // Failure-detection test hook (w4a4_test_fault): while bit 0 is set, the
 // activation-prep producer issues no row copies, so its consumers' waits run
-// out.  Bit 2 makes the e4m3 products and the expert kernel copy no activation
-// tiles (a kernel argument, set by the host).  Zero in normal use.
-enum : uint32_t { FAULT_PREP_SKIP_LOADS = 1u << 0, FAULT_FP8_SKIP_ACTS = 1u << 2 };
+// out.  Zero in normal use.
+enum : uint32_t { FAULT_PREP_SKIP_LOADS = 1u << 0 };
 static __device__ uint32_t g_fault_mask = 0u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -44,8 +44,6 @@ __host__ __device__ __forceinline__ int64_t sf_offset(int64_t r, int64_t b, int6
 }
 
 int device_num_sms();
-// the mask last given to w4a4_test_fault
-uint32_t host_fault_mask();
 
 // Launch attributes of a kernel that calls pdl_wait() before its first
 // global-memory access: programmatic dependent launch, so its launch and
