@@ -20,6 +20,7 @@
 //  * fp8_gemm_mid_kernel: where tiles of 256 x 256 would leave most SMs idle:
 //    128 tokens x 256 channels per CTA, K split and joined in the same way.
 // Every wait is bounded, as in the other kernels of the library.
+#include <atomic>
 #include <cuda.h>
 
 #include "fp8_device.cuh"
@@ -737,13 +738,16 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      // What bounds the kernel: the chain through a buffer.  Its MMAs run 512
-      // cycles (560 a K block measured without this loop: 190 us at T = 4096,
-      // 5120 -> 13824), then commit, this warp's look (120), loads and arrival
-      // (250), the issuer's look (165) and its issuing (200) follow one another;
-      // with two buffers that makes about 850 cycles a K block (260 us).  The
-      // additions themselves take 330 (100 FMAs per cycle and SM).  Measured and
-      // no faster: 16 warps of 64 columns (268 us), MMAs of 128 columns with a
+      // What bounds the kernel: these warps.  A K block takes 744 cycles (T = 16384,
+      // 13824 -> 5120; and a tile's end 3700 more, so 803 with the 40 K blocks of
+      // T = 4096, 5120 -> 13824), its MMAs 512.  Delays of 100, 200, 400 cycles
+      // before the arrival below cost 136, 218, 406 cycles a K block, all of
+      // them; in the issuer, between its looks and its MMAs, 37, 92, 268.  With one
+      // addition in eight a K block takes 590: the additions (330 at 100 FMAs per
+      // cycle and SM) are half hidden, the rest is the chain of one warp (look,
+      // scale, load, load, arrival), of which a scheduler has two to run.  The power
+      // limit holds the SMs at 1.47 and 1.56 GHz meanwhile.  Measured and no
+      // faster: 16 warps of 64 columns (268 us, this 260), MMAs of 128 columns with a
       // buffer pair per half (267), 32-column loads (262 to 276), scalar FMAs
       // (283), the next block's loads before the last additions (299), the
       // issuer's looks ahead of its MMAs (276).  A wait that fails (it ends in
@@ -853,14 +857,15 @@ __global__ void __launch_bounds__(Q_THREADS, 1)
 // kFewSplits, once per device.
 template <int N>
 static cudaError_t few_fits(const int** fits) {
-  static int cached[64][kFewMaxSplit + 1] = {{0}};      // [0]: filled
+  static int cached[64][kFewMaxSplit + 1] = {{0}};
+  static std::atomic<int> filled[64];        // (threads that fill it at once write the same numbers)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int* n = cached[dev];
   *fits = n;
-  if (n[0]) return cudaSuccess;
+  if (filled[dev].load(std::memory_order_acquire)) return cudaSuccess;
   const size_t smem = sizeof(FewSmem<N>) + 1024;
   e = cudaFuncSetAttribute(fp8_gemm_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem));
@@ -885,7 +890,7 @@ static cudaError_t few_fits(const int** fits) {
     if (e != cudaSuccess) return e;
     n[c] = fp8_clusters_that_fit(fit, counted, F_PER_SM);
   }
-  n[0] = 1;
+  filled[dev].store(1, std::memory_order_release);
   return cudaSuccess;
 }
 
