@@ -29,9 +29,9 @@
 //    run at once.
 //
 // Measured (back to back, three sets of weights in turn): 64 tokens, 64 experts
-// of 5120 x 1536, 8 chosen: 272 us, 5.55 TB/s of the weights met; 16 tokens, 128
-// experts of 2048 x 768, 8 chosen: 71 us, 5.5 TB/s; 1 token, 2 of 8 experts of
-// 5120 x 13824: 79 us, 5.4 TB/s; 1 token, 6 of 64 experts of 2048 x 1024: 26 us,
+// of 5120 x 1536, 8 chosen: 292 us, 5.2 TB/s of the weights met; 16 tokens, 128
+// experts of 2048 x 768, 8 chosen: 75 us, 5.2 TB/s; 1 token, 2 of 8 experts of
+// 5120 x 13824: 80 us, 5.3 TB/s; 1 token, 6 of 64 experts of 2048 x 1024: 26 us,
 // of which the router takes 5.5 and the chain route -> up -> down -> y the rest
 // (about ten round trips to memory one after the other).
 // What brought it there: the finishing warps beside the epilogue (64 tokens 787
@@ -76,8 +76,8 @@ __device__ __forceinline__ void cluster_wait() {
 // float32 sum's rounding would change places, and with them whole experts.  So
 // logits are summed in 64 bits, where the products of bf16 numbers are exact
 // and their sums nearly always are.  Layer, us, against float32 sums: 1 token, 6 of
-// 64 experts of 2048 x 1024 25.9, 25.8; 16 tokens, 8 of 128 of 2048 x 768 74.2,
-// 77.0; 64 tokens, 16 of 512 of 2048 x 256 219, 238.  The conversions bound it there;
+// 64 experts of 2048 x 1024 25.8, 25.7; 16 tokens, 8 of 128 of 2048 x 768 74.2,
+// 75.2; 64 tokens, 16 of 512 of 2048 x 256 220, 236.  The conversions bound it there;
 // moving the bits into a double's fields instead was no faster.
 __device__ __forceinline__ void dot8(const uint4& x, const uint4& w0, const uint4& w1, bool two,
                                      double (&acc0)[4], double (&acc1)[4]) {
@@ -111,8 +111,13 @@ struct Steps {
 // each; the width is split where there are fewer pairs of experts than warps);
 // the sums go to the shared memory of the cluster's first CTA, which adds the
 // ranges in order and selects.
+// U: steps of 256 columns whose loads are in flight together.  Four take 96
+// registers, one CTA per SM, which is enough for few tokens; two take 68.  Layer,
+// us, with U = 4 and 2: 1 token, 64 experts 25.7, 26.4; 9 tokens, 64 experts 52.0,
+// 52.4; 16 tokens, 128 experts 77.0, 75.2; 24 tokens, 32 experts 97.2, 95.6.
+constexpr int R_FEW_TOKENS = 12;
+template <int U>
 __global__ void __launch_bounds__(R_THREADS) moe_route_kernel(const __grid_constant__ MoeArgs a) {
-  constexpr int U = 4;                 // steps of 256 columns whose loads are in flight together
   __shared__ double part[kMoeMaxE];            // [split][expert]: more than one split only where E <= 64
   __shared__ double logits[kMoeMaxE];
   __shared__ alignas(16) uint32_t key[kMoeMaxE], key_lo[kMoeMaxE];
@@ -1061,7 +1066,8 @@ cudaError_t run_moe(const MoePlan& p, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1 + static_cast<unsigned>(pdl_attrs(&attr[1]));
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_route_kernel, p.a);
+  void (*route)(MoeArgs) = p.a.T <= R_FEW_TOKENS ? moe_route_kernel<4> : moe_route_kernel<2>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, route, p.a);
   if (e != cudaSuccess) return e;
   if (p.gated)
     return p.n == 16 ? run_moe_experts<16, true>(p, stream)
